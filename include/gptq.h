@@ -482,9 +482,11 @@ typedef struct gptq_experts {
  *              first I columns are the gate's, the others up's
  *   out[t]   = sum_j c[t, j] * (h . Wdown[e_j])         down [I -> H]
  * x, out [T, H] and w_router [E, H] are fp16 or bf16 (x_type).  A GPTQ weight
- * is rounded to x's type as gptq_dequant does; h is carried as two 16-bit parts
- * (with fp16 GPTQ weights |h| beyond 65504 overflows, as fp16 does); sums are
- * fp32, out is rounded once, and repeats are bit-identical.
+ * is rounded to x's type as gptq_dequant does; h enters the down product as two
+ * 16-bit parts: 16 bits of each value in bf16, 22 in fp16 (GPTQ down weights of
+ * fp16 tokens) under a power-of-two scale per row, so that neither small nor
+ * large ones leave fp16's range; sums are fp32, out is rounded once, and repeats
+ * are bit-identical.
  * H % 32 == 0, I % 32 == 0, 1 <= k <= min(E, 16), E <= 1024, each expert's
  * matrix below 2^31 elements; x, w_router, out 16-byte aligned.  Tokens are
  * taken 64 at a time, each time reading the reached experts' weights: it is

@@ -63,8 +63,10 @@ def route(x, w_router, k, renorm):
 def moe_layer(x, w_router, k, w_gate_up, w_down, renorm, out_eps):
     """(out, error bound) for x [T, H], w_gate_up [E, 2I, H], w_down [E, H, I] in fp64.
 
-    The bound counts fp32 sums, h held in two 16-bit parts (2^-15), the fp32
-    silu and router weights (2^-20) and the output's rounding (out_eps / 2)."""
+    The bound counts fp32 sums, h held in two 16-bit parts (2^-15 of each value
+    in bf16; in fp16, under the row's scale, 2^-22 and 2^-38 of the row's
+    largest), the fp32 silu and router weights (2^-20) and the output's rounding
+    (out_eps / 2)."""
     ids, c = route(x, w_router, k, renorm)
     T, H = x.shape
     I = w_down.shape[2]
@@ -77,7 +79,7 @@ def moe_layer(x, w_router, k, w_gate_up, w_down, renorm, out_eps):
             dg, du = (sum_error(H) * mag)[:I], (sum_error(H) * mag)[I:]
             s = g / (1 + np.exp(-g))
             h = s * u
-            dh = 1.1 * dg * (np.abs(u) + du) + np.abs(s) * du + np.abs(h) * 2.0 ** -15 + 2.0 ** -24
+            dh = 1.1 * dg * (np.abs(u) + du) + np.abs(s) * du + np.abs(h) * 2.0 ** -15 + np.abs(h).max() * 2.0 ** -38
             y = wd @ h
             out[t] += c[t, j] * y
             err[t] += c[t, j] * (np.abs(wd) @ dh + (sum_error(I) + 2.0 ** -20) * (np.abs(wd) @ (np.abs(h) + dh)))

@@ -1,13 +1,14 @@
-// A whole mixture-of-experts layer for a few tokens, in three kernels:
+// A whole mixture-of-experts layer for a few tokens, in three kernels (four where
+// fp16 hidden values are split first, see row_scale):
 //   router    a workgroup per token: its logits in fp64, the k best experts
 //             and their weights
 //   gate_up   per expert and column tile: gate and up columns of the same
-//             outputs in one workgroup, so silu(gate) * up needs no exchange;
-//             the router's weight is folded into the hidden values
-//   down      per column tile, over all reached experts one after the other:
-//             every token is a row, so the sum over a token's experts is the
-//             sum over k of one long product, kept in fp32 registers and
-//             rounded once; no partial results, no fourth kernel
+//             outputs in one workgroup, so silu(gate) * up needs no exchange
+//   down      per column tile, over all reached experts one after the other: an
+//             expert's sums are added, times the router's weights, to a table
+//             [token][column] in LDS, fp32; with several workgroups along the
+//             experts their tables go through memory and the last to arrive adds
+//             them.  Rounded once
 // A (token, rank) pair p = t * k + j owns a row of h.  Which tokens an expert
 // has, each workgroup finds for itself in the T * k choices (at most 1024), so
 // the kernels exchange nothing but those arrays.  The products are the
@@ -178,23 +179,147 @@ __device__ __forceinline__ void place_columns(W* w, const ExpertStack& s, int N,
   }
 }
 
-// A weighted hidden value as two parts: the 16-bit value and the 16-bit rest.
-// In bf16 for MXFP4 down weights (exact in bf16, whatever x's type), in x's
-// type for GPTQ ones.  One part alone would add a rounding as large as the
-// output's own.
-template <bool HBF16> __device__ __forceinline__ void split_store(uint16_t* hi, uint16_t* lo, float v) {
-  if constexpr (HBF16) {
-    const uint32_t p = bf16_pair(v, 0.f) & 0xFFFFu;
-    const float top = bf16_to_f32(p);
-    *hi = (uint16_t)p;
-    *lo = (uint16_t)(bf16_pair(__builtin_isinf(top) ? 0.f : v - top, 0.f) & 0xFFFFu);
-  } else {
-    const _Float16 p = (_Float16)v;
-    const float rest = v - (float)p;
-    *hi = __builtin_bit_cast(uint16_t, p);
-    *lo = __builtin_bit_cast(uint16_t, (_Float16)(__builtin_isinf((float)p) ? 0.f : rest));
-  }
+// A hidden value enters the down product as two parts, the 16-bit value and the
+// 16-bit rest: one part alone would add a rounding as large as the output's own.
+// Where the down weights are exact in bf16 (bf16 GPTQ, and MXFP4 whatever x's
+// type) the parts are bf16, split here: 16 bits of the value, at fp32's range.
+__device__ __forceinline__ void split_store(uint16_t* hi, uint16_t* lo, float v) {
+  const uint32_t p = bf16_pair(v, 0.f) & 0xFFFFu;
+  const float top = bf16_to_f32(p);
+  *hi = (uint16_t)p;
+  *lo = (uint16_t)(bf16_pair(__builtin_isinf(top) ? 0.f : v - top, 0.f) & 0xFFFFu);
 }
+// fp16 GPTQ down weights need fp16 parts, whose range (2^-24 .. 65504) hidden
+// values leave on both sides.  So h stays fp32 in memory, beside the largest
+// magnitude of each pair's row in every column tile, and is split under the power
+// of two that puts a row's largest into 2^14 .. 2^15 (at most 2^60): 22 bits of
+// every value, or 2^-39 of the row's largest.  The flush undoes the scale.  (A
+// value per tile and not one raised by atomics: one token over 64 experts of 2048
+// x 1024, gate_up 9.5 us and 13.5, 64 atomics meeting at an address.)
+// Row blocks of up to kWideRows rows are split by the down product in LDS, every
+// column tile anew; more rows by a kernel of its own first (us for the layer,
+// without it and with it: one token, 64 experts of 2048 x 1024, k 8, 27.8 and
+// 30.9; four tokens 50 and 52; 16 tokens, 8 experts of 4096 x 14336, k 2, 245
+// and 220; 64 tokens, 16 experts of 2048 x 2048, k 16, 443 and 279).
+constexpr int kWideRows = 4;
+constexpr int kTopExponent = 14, kMostScale = 60;
+__device__ __forceinline__ int row_scale(uint32_t top) {
+  return min(kTopExponent + 127 - (int)(top >> 23), kMostScale);
+}
+// two values under a scale as two parts; the second is at most 8, beside an
+// infinity it is NaN, which becomes -64
+__device__ __forceinline__ void split_wide(float a, float b, float scale, uint32_t* hi, uint32_t* lo) {
+  const half2_t h = {(_Float16)__builtin_fmaf(a, scale, 0.f), (_Float16)__builtin_fmaf(b, scale, 0.f)};
+  const half2_t l = {(_Float16)__builtin_fmaf(a, scale, -(float)h[0]), (_Float16)__builtin_fmaf(b, scale, -(float)h[1])};
+  *hi = as_u32(h);
+  *lo = as_u32(__builtin_elementwise_max(l, half2_t{(_Float16)-64.f, (_Float16)-64.f}));
+}
+__device__ __forceinline__ float scale_of(int exponent) { return __uint_as_float((uint32_t)(127 + exponent) << 23); }
+
+// Every pair's row split once, eight values a thread; the router's weight takes
+// the inverse of the scale.
+__global__ __launch_bounds__(256) void moe_split_kernel(MoeArgs a) {
+  __shared__ uint32_t top[4];
+  const int pairs = a.T * a.k, parts = (a.I + 2047) / 2048;
+  const int p = (int)blockIdx.x / parts, i = ((int)blockIdx.x % parts * 256 + (int)threadIdx.x) * 8;
+  const float* h = static_cast<const float*>(a.h) + (int64_t)p * a.I + i;
+  floatx4_t f[2] = {};
+  if (i < a.I) {
+    f[0] = *reinterpret_cast<const floatx4_t*>(h);
+    f[1] = *reinterpret_cast<const floatx4_t*>(h + 4);
+  }
+  uint32_t m = 0;
+  for (int t = threadIdx.x; t < a.up_tiles; t += 256) m = max(m, a.top[t * pairs + p]);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+  if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
+  __syncthreads();
+  const int s = row_scale(max(max(top[0], top[1]), max(top[2], top[3])));
+  if (i == 0) a.weight[p] = ldexpf(a.weight[p], -s);
+  if (i >= a.I) return;
+  u32x4_t hi, lo;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t x, y;
+    split_wide(f[v >> 1][2 * (v & 1)], f[v >> 1][2 * (v & 1) + 1], scale_of(s), &x, &y);
+    hi[v] = x;
+    lo[v] = y;
+  }
+  uint16_t* out = a.split_h + (int64_t)p * a.I + i;
+  *reinterpret_cast<u32x4_t*>(out) = hi;
+  *reinterpret_cast<u32x4_t*>(out + (int64_t)pairs * a.I) = lo;
+}
+
+// largest of the 16 lanes of a row of lanes, in each of them
+__device__ __forceinline__ uint32_t max16(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));    // lanes 1 0 3 2
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));    // lanes 2 3 0 1
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));   // lanes 7 .. 0
+  return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xF, 0xF, true));  // lanes 15 .. 0
+}
+
+// Rows of fp32 in LDS, row r `kp` k in chunks of 256 (1 KB): loaded as they are,
+// then split in place, a chunk by one wave: the parts 0, then the parts 1, 512
+// bytes each, 16-byte pieces (eight k) of row r at slot p ^ (r % 16).  (Splitting
+// in the operand reads takes every column wave 20 instructions per 32 k: one
+// token over 64 experts of 2048 x 1024, 4-bit, down 13.7 us, here 10.7.)
+struct WideRows {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int rows, K, kp;                   // kp a power of two, 256 at least
+
+  // k [k0, k0 + kp) of every row into lds; lane r of `off` holds row r's byte
+  // offset; k >= min(K, end) reads zero
+  __device__ __forceinline__ void issue(int k0, int end, uint8_t* lds, uint32_t off, int wave, int nw, int lane) const {
+    const int stop = min(K, end), lg = __builtin_ctz(kp) - 8;
+    for (int i = wave; i < rows << lg; i += nw) {
+      const uint32_t base = (uint32_t)__builtin_amdgcn_readlane((int)off, i >> lg);
+      const int k = k0 + 256 * (i & ((1 << lg) - 1)) + 4 * lane;
+      dma16(rsrc, lds + 1024 * i, k < stop ? base + 4u * (uint32_t)k : kPast);
+    }
+  }
+  // lane r of `e` holds the exponent of row r's scale; four chunks' reads at once
+  __device__ __forceinline__ void split(uint8_t* lds, int e, int wave, int nw, int lane) const {
+    constexpr int U = 4;
+    const int lg = __builtin_ctz(kp) - 8, chunks = rows << lg;
+    const int to = 16 * (lane >> 1) + 8 * (lane & 1);
+    for (int i0 = wave; i0 < chunks; i0 += U * nw) {
+      floatx4_t f[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * nw < chunks) f[u] = *reinterpret_cast<const floatx4_t*>(lds + 1024 * (i0 + u * nw) + 16 * lane);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * nw, r = i >> lg;
+        if (i >= chunks) break;
+        const float scale = scale_of(__builtin_amdgcn_readlane(e, r));
+        u32x2_t hi, lo;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          uint32_t x, y;
+          split_wide(f[u][2 * v], f[u][2 * v + 1], scale, &x, &y);
+          hi[v] = x;
+          lo[v] = y;
+        }
+        uint8_t* at = lds + 1024 * i + (to ^ (16 * (r & 15)));
+        *reinterpret_cast<u32x2_t*>(at) = hi;
+        *reinterpret_cast<u32x2_t*>(at + 512) = lo;
+      }
+    }
+  }
+};
+
+// Operand reads of one unit from split rows (one row tile; an absent row reads
+// row 0).  `row`: the unit's first piece, a multiple of 16 within the row.
+template <class W> struct WideOperand {
+  const uint8_t* lds;
+  const W& w;
+  uint32_t row, swz;
+  __device__ __forceinline__ half8_t operator()(int, int pl, int s) const {
+    const uint32_t p = w.piece(s);
+    return *reinterpret_cast<const half8_t*>(lds + row + 1024u * (p >> 5) + 256u * (p >> 4 & 1u) + 512u * (uint32_t)pl +
+                                             16u * ((p & 15u) ^ swz));
+  }
+};
 
 // Rows of one expert beyond a row block's are taken by further workgroups.  Workgroup
 // (slot, row block, tile): with no fewer pairs than experts a slot is an
@@ -205,6 +330,7 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ int pair_of[16 * MT];
   __shared__ uint32_t off[16 * MT];
+  __shared__ uint32_t top[16 * MT];                // bits of the rows' largest |h| (fp32 h)
   constexpr int CT = 2 * CS;
   typedef typename WeightsOf<FMT, TILED, BF16, CS, CT, ONE>::type W;
   const MoeShape& g = a.up_shape;
@@ -262,6 +388,7 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs a) {
   const int rows = min(B, count - rb * B);
   if (rows <= 0) return;
   if (!early) w.load(kw, mine && kw < units, weights(0), &r0);
+  if (!HBF16 && threadIdx.x < 16 * MT) top[threadIdx.x] = 0;
   __syncthreads();
   const int nmt = (rows + 15) >> 4;
   StagedRows x;
@@ -302,7 +429,7 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs a) {
     if (p + 2 < phases) issue(p + 2, &r0);
     compute(p + 1, r1);
   }
-  // the k waves' sums, then silu(gate) * up * weight
+  // the k waves' sums, then silu(gate) * up
   floatx4_t* red = reinterpret_cast<floatx4_t*>(lds);
   if (g.nwk > 1) {
     __syncthreads();
@@ -314,40 +441,53 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs a) {
     }
     __syncthreads();
   }
-  if (!mine) return;
-  uint16_t* hi = a.h;
-  uint16_t* lo = a.h + (int64_t)pairs * a.I;
+  uint16_t* hi = static_cast<uint16_t*>(a.h);
+  uint16_t* lo = hi + (int64_t)pairs * a.I;
+  if (mine) {
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    if (mt >= nmt) break;
+    for (int mt = 0; mt < MT; ++mt) {
+      if (mt >= nmt) break;
 #pragma unroll
-    for (int j = 0; j < CS; ++j) {
-      if ((mt * CS + j) % g.nwk != kw) continue;
-      floatx4_t gate = acc[mt][j], up = acc[mt][CS + j];
-      if (g.nwk > 1) {
-        gate = up = floatx4_t{0.f, 0.f, 0.f, 0.f};
-        for (int k = 0; k < g.nwk; ++k) {
-          gate += red[((k * g.nwc + cw) * MT * CT + mt * CT + j) * 64 + lane];
-          up += red[((k * g.nwc + cw) * MT * CT + mt * CT + CS + j) * 64 + lane];
+      for (int j = 0; j < CS; ++j) {
+        if ((mt * CS + j) % g.nwk != kw) continue;
+        floatx4_t gate = acc[mt][j], up = acc[mt][CS + j];
+        if (g.nwk > 1) {
+          gate = up = floatx4_t{0.f, 0.f, 0.f, 0.f};
+          for (int k = 0; k < g.nwk; ++k) {
+            gate += red[((k * g.nwc + cw) * MT * CT + mt * CT + j) * 64 + lane];
+            up += red[((k * g.nwc + cw) * MT * CT + mt * CT + CS + j) * 64 + lane];
+          }
         }
-      }
-      const int m = 16 * mt + 4 * (lane >> 4), n = column_of<FMT, TILED, CS>(n0, j, lane & 15);
+        const int m = 16 * mt + 4 * (lane >> 4), n = column_of<FMT, TILED, CS>(n0, j, lane & 15);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (m + i < rows) {
-          const int p = pair_of[m + i];
-          const int64_t o = (int64_t)p * a.I + n;
-          split_store<HBF16>(hi + o, lo + o, gate[i] / (1.f + expf(-gate[i])) * up[i] * a.weight[p]);
+        for (int i = 0; i < 4; ++i) {
+          if (m + i < rows) {
+            const int64_t o = (int64_t)pair_of[m + i] * a.I + n;
+            const float v = gate[i] / (1.f + expf(-gate[i])) * up[i];
+            if constexpr (HBF16) {
+              split_store(hi + o, lo + o, v);
+            } else {
+              static_cast<float*>(a.h)[o] = v;
+              const uint32_t most = max16(__float_as_uint(v) & 0x7FFFFFFFu);
+              if ((lane & 15) == 0) atomicMax(&top[m + i], most);
+            }
+          }
         }
       }
     }
+  }
+  if constexpr (!HBF16) {
+    __syncthreads();
+    if ((int)threadIdx.x < rows) a.top[tile * pairs + pair_of[threadIdx.x]] = top[threadIdx.x];
   }
 }
 
 // Workgroup (split, tile): phases (expert, row block, part of I) in expert
 // order, a consecutive share of all units per workgroup.  A wave's sums of one
-// expert's rows are added to its LDS table [token][column] before the next.
-template <int FMT, bool TILED, bool BF16, int CS, bool ONE>
+// expert's rows are added, times the router's weights, to its LDS table
+// [token][column] before the next.
+// WIDE: h is fp32 and split here.
+template <int FMT, bool TILED, bool BF16, int CS, bool ONE, bool WIDE>
 __global__ __launch_bounds__(512, 2) void moe_down_kernel(MoeArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ int count[kMaxExperts];               // pairs of an expert, then its first sorted pair
@@ -355,6 +495,9 @@ __global__ __launch_bounds__(512, 2) void moe_down_kernel(MoeArgs a) {
   __shared__ int16_t first[kMaxExperts + 1];       // first sorted pair of each of them
   __shared__ int16_t sorted[kMaxPairs], place[kMaxPairs];
   __shared__ int flag;
+  static_assert(kMaxPairs <= kMaxExperts, "factor in count's place");
+  float* factor = reinterpret_cast<float*>(count); // once sorted: what a pair's sums are multiplied by,
+  int16_t* scale = place;                          // and the exponent of its row's scale (WIDE)
   constexpr int MT = 1;
   typedef typename WeightsOf<FMT, TILED, BF16, CS, CS, ONE>::type W;
   const MoeShape& g = a.down_shape;
@@ -366,11 +509,16 @@ __global__ __launch_bounds__(512, 2) void moe_down_kernel(MoeArgs a) {
   const int cw = wave % g.nwc, kw = wave / g.nwc;
   const int n0 = tile * cols + 16 * CS * cw;
   const bool mine = n0 < a.H;
+  // used once the pairs are sorted, loaded beside what the sort waits for
+  const int tops = WIDE ? pairs * a.up_tiles : 0;
+  const uint32_t first_top = tid < tops ? a.top[tid] : 0u;
+  const float first_weight = tid < pairs ? a.weight[tid] : 0.f;
 
   // pairs sorted by expert (within one in any order: rows do not mix)
   if (pairs <= 64) {
     // few: every lane counts what comes before its pair
     if (wave == 0) {
+      count[lane] = 0;
       const int e = lane < pairs ? a.chosen[lane] : kMaxExperts;
       int before_pair = 0, before_expert = 0;
       bool again = false;
@@ -427,6 +575,23 @@ __global__ __launch_bounds__(512, 2) void moe_down_kernel(MoeArgs a) {
     }
     __syncthreads();
     for (int p = tid; p < pairs; p += blockDim.x) sorted[count[a.chosen[p]] + place[p]] = (int16_t)p;
+    __syncthreads();                               // count and place are free
+    if (WIDE) {
+      for (int p = tid; p < pairs; p += blockDim.x) count[p] = 0;
+      __syncthreads();
+    }
+  }
+  if (WIDE) {
+    auto raise = [&](int i, uint32_t top) __attribute__((always_inline)) { atomicMax(&count[i % pairs], (int)top); };
+    if (tid < tops) raise(tid, first_top);
+    for (int i = tid + blockDim.x; i < tops; i += blockDim.x) raise(i, a.top[i]);
+    __syncthreads();
+  }
+  for (int p = tid; p < pairs; p += blockDim.x) {
+    const float c = p == tid ? first_weight : a.weight[p];
+    const int s = WIDE ? row_scale((uint32_t)count[p]) : 0;
+    factor[p] = WIDE ? ldexpf(c, -s) : c;
+    scale[p] = (int16_t)s;
   }
   const int experts = __builtin_amdgcn_readfirstlane(flag);
 
@@ -438,12 +603,13 @@ __global__ __launch_bounds__(512, 2) void moe_down_kernel(MoeArgs a) {
   float* table = reinterpret_cast<float*>(lds + 2 * phase + kw * tokens);
   for (int i = tid; i < g.nwk * a.T * cols; i += blockDim.x) reinterpret_cast<float*>(lds + 2 * phase)[i] = 0.f;
   uint32_t* off = reinterpret_cast<uint32_t*>(lds + 2 * phase + g.nwk * tokens);    // [2][B]
+  int exponents[2] = {0, 0};                       // lane r: of row r's scale, per buffer (WIDE)
   auto weights = [&](int b) __attribute__((always_inline)) { return lds + b * phase + wave * W::BYTES; };
   auto rows_at = [&](int b) __attribute__((always_inline)) { return lds + b * phase + wbytes; };
   const uint32_t plane = (uint32_t)pairs * (uint32_t)a.I * 2u;
-  StagedRows x;
-  x.rsrc = buffer_of(a.h, 2u * plane);
-  x.plane = plane;
+  typename std::conditional<WIDE, WideRows, StagedRows>::type x;
+  x.rsrc = buffer_of(BF16 || WIDE ? a.h : a.split_h, 2u * plane);
+  if constexpr (!WIDE) x.plane = plane;
   x.K = a.I;
   x.kp = kp;
   floatx4_t acc[MT][CS];
@@ -489,38 +655,46 @@ __global__ __launch_bounds__(512, 2) void moe_down_kernel(MoeArgs a) {
   auto issue = [&](const Phase& p, int b, typename W::Regs* r) __attribute__((always_inline)) {
     bind_expert<FMT, W>(&w, a.down, __builtin_amdgcn_readfirstlane(reached[p.slot]), a.H, a.I);
     w.load(p.unit + kw, mine && p.unit + kw < p.end, weights(b), r);
-    // every wave writes the same offsets (its own lanes read them back)
-    if (lane < p.rows) off[b * B + lane] = (uint32_t)sorted[p.base + lane] * (uint32_t)a.I * 2u;
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    x.off = off + b * B;
-    x.rows = p.rows;
-    x.template issue<2>(p.unit * W::KU, p.end * W::KU, rows_at(b), wave, nw, lane);
+    if constexpr (WIDE) {
+      const int q = lane < p.rows ? sorted[p.base + lane] : 0;
+      exponents[b] = scale[q];
+      x.rows = p.rows;
+      x.issue(p.unit * W::KU, p.end * W::KU, rows_at(b), (uint32_t)q * (uint32_t)a.I * 4u, wave, nw, lane);
+    } else {
+      // every wave writes the same offsets (its own lanes read them back)
+      if (lane < p.rows) off[b * B + lane] = (uint32_t)sorted[p.base + lane] * (uint32_t)a.I * 2u;
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      x.off = off + b * B;
+      x.rows = p.rows;
+      x.template issue<2>(p.unit * W::KU, p.end * W::KU, rows_at(b), wave, nw, lane);
+    }
   };
   auto compute = [&](const Phase& p, int b, const typename W::Regs& r) __attribute__((always_inline)) {
     if (!mine || p.unit + kw >= p.end) return;
     const uint32_t swz = (uint32_t)((lane & 15) < p.rows ? lane & 15 : 0);
-    UnitOperand<W, MT> operand{rows_at(b), w, {}, swz, (uint32_t)(p.rows * kp * 2), kw * (W::KU / 8)};
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int m = 16 * mt + (lane & 15);
-      operand.row[mt] = (uint32_t)(m < p.rows ? m : (int)swz) * kp * 2u;
+    if constexpr (WIDE) {
+      const uint32_t first = (uint32_t)kw * (W::KU / 8);
+      const WideOperand<W> operand{rows_at(b), w, swz * kp * 4u + 1024u * (first >> 5) + 256u * (first >> 4 & 1u), swz};
+      w.template multiply<MT, 2>(weights(b), r, p.unit + kw, operand, 1, acc);
+    } else {
+      UnitOperand<W, MT> operand{rows_at(b), w, {swz * kp * 2u}, swz, (uint32_t)(p.rows * kp * 2), kw * (W::KU / 8)};
+      w.template multiply<MT, 2>(weights(b), r, p.unit + kw, operand, 1, acc);
     }
-    w.template multiply<MT, 2>(weights(b), r, p.unit + kw, operand, (p.rows + 15) >> 4, acc);
   };
   // the rows of phase p are complete: add them to their tokens
   auto flush = [&](const Phase& p) __attribute__((always_inline)) {
     if (mine) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int i = 0; i < 4; ++i) {
+        const int m = 4 * (lane >> 4) + i;
+        if (m < p.rows) {
+          const int q = sorted[p.base + m];
+          const float f = factor[q];
+          float* t = table + (q / a.k) * cols + 16 * CS * cw;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = 16 * mt + 4 * (lane >> 4) + i;
-          if (m < p.rows) {
-            float* t = table + (sorted[p.base + m] / a.k) * cols + 16 * CS * cw;
-#pragma unroll
-            for (int j = 0; j < CS; ++j) t[column_of<FMT, TILED, CS>(0, j, lane & 15)] += acc[mt][j][i];
-          }
+          for (int j = 0; j < CS; ++j) t[column_of<FMT, TILED, CS>(0, j, lane & 15)] += acc[0][j][i] * f;
         }
+      }
     }
     clear();
   };
@@ -535,6 +709,14 @@ __global__ __launch_bounds__(512, 2) void moe_down_kernel(MoeArgs a) {
       const bool more = advance(&next);
       phase_ready();
       if (more) issue(next, b ^ 1, then);
+      if constexpr (WIDE) {                        // the next phase's loads are under way
+        x.rows = cur.rows;
+        x.split(rows_at(b), exponents[b], wave, nw, lane);
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      }
       compute(cur, b, now);
       if (!more || next.slot != cur.slot || next.rb != cur.rb) flush(cur);
       cur = next;
@@ -654,7 +836,12 @@ size_t plan_moe(MoeArgs* a, char* base, size_t* counter_bytes) {
   };
   a->chosen = reinterpret_cast<int32_t*>(take(P * 4));
   a->weight = reinterpret_cast<float*>(take(P * 4));
-  a->h = reinterpret_cast<uint16_t*>(take(2 * P * (size_t)a->I * 2));
+  a->up_tiles = (a->I + uc * u.nwc - 1) / (uc * u.nwc);
+  a->top = reinterpret_cast<uint32_t*>(take(P * (size_t)a->up_tiles * 4));
+  a->h = take(P * (size_t)a->I * 4);
+  const bool fp16_parts = !a->bf16 && a->down.bits != 0;
+  a->split_first = fp16_parts && d.block_rows > kWideRows;
+  a->split_h = reinterpret_cast<uint16_t*>(take(a->split_first ? P * (size_t)a->I * 4 : 0));
   a->part = reinterpret_cast<float*>(take(d.splits > 1 ? (size_t)d.splits * T * (size_t)a->H * 4 : 0));
   return off;
 }
@@ -687,7 +874,7 @@ hipError_t gate_up_typed(const MoeArgs& a, hipStream_t stream) {
   return hipErrorInvalidValue;
 }
 
-template <int FMT, bool TILED, bool BF16> hipError_t down_typed(const MoeArgs& a, hipStream_t stream) {
+template <int FMT, bool TILED, bool BF16, bool WIDE> hipError_t down_typed(const MoeArgs& a, hipStream_t stream) {
   constexpr int CS = segment_tiles(FMT, TILED);
   const MoeShape& g = a.down_shape;
   const int cols = 16 * CS * g.nwc;
@@ -695,9 +882,9 @@ template <int FMT, bool TILED, bool BF16> hipError_t down_typed(const MoeArgs& a
   const size_t lds = down_lds(a);
   const int unit = unit_of(a.down, 1);
   if (FMT == 0 || a.down.group_size % 128 == 0)
-    return launch_shaped(moe_down_kernel<FMT, TILED, BF16, CS, true>, grid, g, unit, lds, a, stream);
+    return launch_shaped(moe_down_kernel<FMT, TILED, BF16, CS, true, WIDE>, grid, g, unit, lds, a, stream);
   if constexpr (FMT != 0)
-    return launch_shaped(moe_down_kernel<FMT, TILED, BF16, CS, false>, grid, g, unit, lds, a, stream);
+    return launch_shaped(moe_down_kernel<FMT, TILED, BF16, CS, false, WIDE>, grid, g, unit, lds, a, stream);
   return hipErrorInvalidValue;
 }
 
@@ -713,9 +900,12 @@ template <int FMT, bool TILED> hipError_t gate_up_format(const MoeArgs& a, hipSt
 }
 template <int FMT, bool TILED> hipError_t down_format(const MoeArgs& a, hipStream_t stream) {
   if constexpr (FMT != 0) {
-    if (!a.bf16) return down_typed<FMT, TILED, false>(a, stream);
+    if (!a.bf16) {
+      return a.split_first ? down_typed<FMT, TILED, false, false>(a, stream)
+                           : down_typed<FMT, TILED, false, true>(a, stream);
+    }
   }
-  return down_typed<FMT, TILED, true>(a, stream);   // MXFP4: bf16 parts whatever x's type
+  return down_typed<FMT, TILED, true, false>(a, stream);   // MXFP4: bf16 parts whatever x's type
 }
 
 template <bool BF16> hipError_t router_typed(const MoeArgs& a, hipStream_t stream) {
@@ -736,6 +926,11 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
   else if (g == 4) err = gt ? gate_up_format<4, true>(a, stream) : gate_up_format<4, false>(a, stream);
   else err = gt ? gate_up_format<8, true>(a, stream) : gate_up_format<8, false>(a, stream);
   if (err != hipSuccess) return err;
+  if (a.split_first) {
+    moe_split_kernel<<<(unsigned)(a.T * a.k * ((a.I + 2047) / 2048)), 256, 0, stream>>>(a);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
   const int d = a.down.bits, dt = a.down.tiled;
   if (d == 0) err = down_format<0, false>(a, stream);
   else if (d == 2) err = dt ? down_format<2, true>(a, stream) : down_format<2, false>(a, stream);

@@ -64,7 +64,12 @@ struct MoeArgs {
   ExpertStack gate_up, down;
   int32_t* chosen;           // [T * k] expert of pair t * k + j
   float* weight;             // [T * k] its weight
-  uint16_t* h;               // [2, T * k, I] weighted hidden values, two 16-bit parts
+  void* h;                   // hidden values: [2, T * k, I] in two bf16 parts, or, before
+                             // fp16 GPTQ down weights, [T * k, I] in fp32
+  uint32_t* top;             // fp32 h: [up_tiles, T * k] bits of the largest |h| of a
+  int up_tiles;              // row in each of gate_up's column tiles
+  int split_first;           // fp32 h goes to split_h [2, T * k, I], two fp16 parts, in
+  uint16_t* split_h;         // a kernel of its own; else the down product splits it
   MoeShape up_shape, down_shape;
   // down product: with several splits per column tile their fp32 sums
   // [splits, T, H] go to part, the last to arrive (counted in cnt[tile], zero

@@ -296,8 +296,9 @@ template <int BITS, bool TILED, bool BF16, int CS, int CT, int UPP, bool ONE> st
           const uint32_t so = (g * (uint32_t)N + (uint32_t)n) * 2u;
           r->z[u][t][0] = load4(qz, ok ? zo : kPast);
           if constexpr (BITS == 3) r->z[u][t][1] = load4(qz, ok && (bit & 31) + 3 * ZC > 32 ? zo + 4u : kPast);
-          if constexpr (ZC == 2) r->s[u][t] = load4(sc, ok ? so : kPast);
-          else r->s[u][t] = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sc, (int)(ok ? so : kPast), 0, 0);
+          // one column: the word that holds it (a 16-bit load is widened where it is
+          // issued, and that waits for every load before it)
+          r->s[u][t] = load4(sc, ok ? so & ~3u : kPast);
         }
       }
     }
@@ -336,7 +337,8 @@ template <int BITS, bool TILED, bool BF16, int CS, int CT, int UPP, bool ONE> st
           if constexpr (BITS == 3) zz = __builtin_amdgcn_alignbit(of_chunk(r.z[u][t][1], s), z0, sh);
           else zz = z0 >> sh;
           const int z = (int)((zz >> (BITS * (j % ZC))) & ((1u << BITS) - 1u)) + zero_offset;
-          const uint32_t sv = (of_chunk(r.s[u][t], s) >> (16 * (j % ZC))) & 0xFFFFu;
+          const int half = ZC == 2 ? j % ZC : col[t] & 1;
+          const uint32_t sv = (of_chunk(r.s[u][t], s) >> (16 * half)) & 0xFFFFu;
           if constexpr (BF16) {
             bs[j] = bf16_to_f32(sv);
             bc[j] = -(float)z * bs[j];
