@@ -119,7 +119,8 @@ __device__ __forceinline__ void mx_tile_body(const MxGemmArgs& a) {
     const uint8_t* sl = stage(st);
     if constexpr (!BF16) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) fits = fits && (mx_fits_f16(ws[s3][j]) || 2 * (kt0 + kt) + h >= w_end);
+      for (int j = 0; j < NT; ++j)
+        fits = fits && (mx_fits_f16(ws[s3][j]) || mx_zero(w[s3][j]) || 2 * (kt0 + kt) + h >= w_end);
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -164,9 +165,10 @@ __device__ __forceinline__ void mx_tile_body(const MxGemmArgs& a) {
   }
 
   if constexpr (!BF16) {
-    // a scale outside fp16's range somewhere in the tile's columns (weights of
-    // ordinary size never meet one): the tile again with the weights in bf16,
-    // which holds every MXFP4 value, and x as two bf16 parts
+    // a scale outside fp16's range, of a block that is not all zeros, somewhere in
+    // the tile's columns (weights of ordinary size never meet one): the tile again
+    // with the weights in bf16, which holds every MXFP4 value, and x as two bf16
+    // parts
     if (__syncthreads_or(fits ? 0 : 1)) {
       clear();
       for (int kt = 0; kt < ktiles; ++kt) {

@@ -125,6 +125,13 @@ template <bool BF16, int CT> struct MxWeights : MxTiles<CT> {
         b[t][j] = this->byte_of(r, t, j, unit);
         fits = fits && mx_fits_f16(b[t][j]);
       }
+    if (!BF16 && !__all(fits)) {                   // ordinary weights do not come here
+      fits = true;
+#pragma unroll
+      for (int t = 0; t < CT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fits = fits && (mx_fits_f16(b[t][j]) || mx_zero(this->block(lds, t, j)));
+    }
     if (!BF16 && !__all(fits)) {
       // a scale outside fp16's range: the block in bf16 (which holds every
       // MXFP4 value), the activations as two bf16 parts
