@@ -92,3 +92,14 @@ def test_nonzero_blocks_beside_zero_ones_keep_their_scale(dev, M):
         scales[n, b] = rng.choice([0, 60, 103, 141, 160])
     y = product(dev, x, codes, scales)
     assert_bound(y, x, codes, scales, K)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K", [(1, 4096), (16, 2080), (20, 4096)])
+@pytest.mark.parametrize("N,more", [(17, 32), (47, 64), (64 + 16, 128)])
+def test_columns_past_the_end_leave_the_path_alone(dev, M, K, N, more):
+    """N off the column tiles: bit for bit the first columns of the product with whole tiles."""
+    _, x, codes, scales = operands(M, more, K, seed=N)
+    y = product(dev, x, codes[:N], scales[:N])
+    assert torch.equal(y, product(dev, x, codes, scales)[:, :N])
+    assert_bound(y, x, codes[:N], scales[:N], K)
