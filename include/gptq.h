@@ -404,7 +404,8 @@ GPTQ_API int gptq_read_ceiling(const void* buf, int64_t bytes, void* sink, void*
  *                            mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6), the even
  *                            k in the low nibble
  *   scales  uint8 [R, K/32]  one byte b per 32 consecutive k: scale 2^(b - 127),
- *                            b = 255: every value of the block is NaN
+ *                            b = 255: every value of the block is NaN; the
+ *                            quantiser makes no byte above 252 but 255
  * K % 32 == 0, K <= 2^20.  codes 16-byte aligned (so are then all its rows).
  */
 typedef enum gptq_type {
@@ -430,8 +431,9 @@ GPTQ_API int gptq_mxfp4_quantize(const void* x, int x_type, int64_t M, int64_t K
 GPTQ_API int gptq_mxfp4_quantize_check(const void* x, int x_type, int64_t M, int64_t K, const uint8_t* codes,
                                        const uint8_t* scales);
 
-/* MXFP4 -> values [M, K] in out_type (fp16, bf16 or fp32; exact in bf16 and
- * fp32, one rounding to nearest even, possibly to infinity, in fp16). */
+/* MXFP4 -> values [M, K] in out_type (fp16, bf16 or fp32), rounded once to
+ * nearest even: exact in bf16 and fp32 for scale bytes up to 252 (values of 2^128
+ * and above, under bytes 253 and 254, become infinities), in fp16 for 104 .. 140. */
 GPTQ_API int gptq_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out,
                                 int out_type, void* stream);
 
@@ -440,8 +442,9 @@ GPTQ_API int gptq_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int
  *   x_type   GPTQ_TYPE_F16 or _BF16 (x_scales NULL), or GPTQ_TYPE_MXFP4 (x is
  *            codes [M, K/2] and x_scales its scales [M, K/32])
  *   out_type fp16, bf16 or fp32: the fp32 sums rounded once
- * Every product is exact; sums are fp32, in an order fixed by the shapes, so
- * repeats are bit-identical.  Any N >= 1; sizes as for gptq_gemm otherwise.
+ * Every product is exact, under any scale; sums are fp32, in an order fixed by
+ * the shapes (and by which scales x's type holds), so repeats are bit-identical.
+ * Any N >= 1; sizes as for gptq_gemm otherwise.
  * x 16-byte aligned, out 4-byte aligned.  Splitting K over workgroups uses the
  * stream's workspace; where it cannot be had (capture before the first call)
  * the call runs unsplit.

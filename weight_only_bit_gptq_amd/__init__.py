@@ -581,8 +581,8 @@ def mxfp4_quantize(x):
 
 
 def mxfp4_dequant(codes, scales, dtype, *, out=None):
-    """Values [..., K] of an MXFP4 tensor in `dtype` (fp16, bf16 or fp32): exact in
-    bf16 and fp32, rounded once in fp16."""
+    """Values [..., K] of an MXFP4 tensor in `dtype` (fp16, bf16 or fp32), rounded once:
+    exact in bf16 and fp32 for scale bytes up to 252, the quantiser's largest."""
     import torch
     kind = _type_code(dtype)
     if kind is None:

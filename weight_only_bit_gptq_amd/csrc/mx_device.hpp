@@ -11,8 +11,10 @@
 // time under a power-of-two scale given as the exponent field of a float.
 // Measured over all 256 codes pairs x 256 scale bytes: decoding equals the
 // format's value rounded to nearest even in the target type (bf16 and fp32
-// hold every value exactly; fp16 does for bytes 104 .. 140), byte 0 is 2^-127
-// and byte 255 gives NaN; encoding rounds to nearest even and saturates at 6.
+// hold every value of bytes up to 252, the quantiser's largest, exactly; under
+// 253 and 254 the large codes pass 2^128 and become infinities; fp16 is exact for
+// bytes 104 .. 140), byte 0 is 2^-127 and byte 255 gives NaN; encoding rounds to
+// nearest even and saturates at 6.
 #pragma once
 
 #include "gptq_device.hpp"
@@ -67,6 +69,23 @@ __device__ __forceinline__ void split_f16(const half8_t& a, half8_t* hi, half8_t
   }
   *hi = __builtin_bit_cast(half8_t, h);
   *lo = __builtin_bit_cast(half8_t, l);
+}
+
+// Under bytes 253 and 254 the large codes are beyond bf16 and fp32.  Where a wave
+// meets such a byte it takes a quarter of all its weights, which bf16 holds
+// exactly, four times (a block left out of some products would add 0 to them, and
+// NaN beside an infinite activation).  No weights of any use come here.
+constexpr uint32_t kMxExact = 252;
+__device__ __forceinline__ bool mx_far(uint32_t byte) { return byte > kMxExact && byte < 255u; }
+// Eight codes in bf16, or a quarter of them.
+__device__ __forceinline__ half8_t mx_frag_bf16(bool quarter, uint32_t w, uint32_t byte) {
+  if (!quarter) return mx_frag<true>(w, mx_scale(byte));
+  const float s = mx_scale(byte == 255u || byte < 4u ? byte : byte - 2u), m = byte < 4u ? 0.25f : 1.f;
+  const f32x2_t v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
+  const f32x2_t v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
+  const u32x4_t r = {bf16_pair(v0[0] * m, v0[1] * m), bf16_pair(v1[0] * m, v1[1] * m), bf16_pair(v2[0] * m, v2[1] * m),
+                     bf16_pair(v3[0] * m, v3[1] * m)};
+  return __builtin_bit_cast(half8_t, r);
 }
 
 template <bool BF16> __device__ __forceinline__ floatx4_t mfma16(const half8_t& a, const half8_t& b, const floatx4_t& c) {

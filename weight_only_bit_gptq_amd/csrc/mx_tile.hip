@@ -101,6 +101,7 @@ __device__ __forceinline__ void mx_tile_body(const MxGemmArgs& a) {
   };
   clear();
   bool fits = true;                                // fp16 x: every scale met lies in fp16's range
+  uint32_t top = 0;                                // bf16 x: the largest scale byte met
 
   // 16 bytes of row 32 i + c at the half's slot of step s
   auto read_x = [&](const uint8_t* sl, int i, int s) __attribute__((always_inline)) {
@@ -117,10 +118,10 @@ __device__ __forceinline__ void mx_tile_body(const MxGemmArgs& a) {
   auto compute = [&](int kt, auto st) __attribute__((always_inline)) {
     constexpr int s3 = decltype(st)::value;
     const uint8_t* sl = stage(st);
-    if constexpr (!BF16) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        fits = fits && (mx_fits_f16(ws[s3][j]) || mx_zero(w[s3][j]) || 2 * (kt0 + kt) + h >= w_end);
+    for (int j = 0; j < NT; ++j) {
+      if (BF16) top = max(top, ws[s3][j]);
+      else fits = fits && (mx_fits_f16(ws[s3][j]) || mx_zero(w[s3][j]) || 2 * (kt0 + kt) + h >= w_end);
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -164,34 +165,37 @@ __device__ __forceinline__ void mx_tile_body(const MxGemmArgs& a) {
     step(kt + 2, S2{}, S1{});
   }
 
-  if constexpr (!BF16) {
-    // a scale outside fp16's range, of a block that is not all zeros, somewhere in
-    // the tile's columns (weights of ordinary size never meet one): the tile again
-    // with the weights in bf16, which holds every MXFP4 value, and x as two bf16
-    // parts
-    if (__syncthreads_or(fits ? 0 : 1)) {
-      clear();
-      for (int kt = 0; kt < ktiles; ++kt) {
-        __syncthreads();
-        load_x(kt, S0{});
-        load_w(kt, S0{});
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
+  // a scale outside the type's range, for fp16 of a block that is not all zeros,
+  // somewhere in the tile's columns (weights of ordinary size never meet one): the
+  // tile again with the weights in bf16 and fp16 x as two bf16 parts
+  if (__syncthreads_or((BF16 ? top <= kMxExact : fits) ? 0 : 1)) {
+    clear();
+    for (int kt = 0; kt < ktiles; ++kt) {
+      __syncthreads();
+      load_x(kt, S0{});
+      load_w(kt, S0{});
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      bool far = false;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          half8_t wv[NT];
+      for (int j = 0; j < NT; ++j) far = far || mx_far(ws[0][j]);
+      far = __any(far);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) wv[j] = mx_frag<true>(w[0][j][s], mx_scale(ws[0][j]));
+      for (int s = 0; s < 4; ++s) {
+        half8_t wv[NT];
 #pragma unroll
-          for (int i = 0; i < MS; ++i) {
-            half8_t hi, lo;
-            split_f16(__builtin_bit_cast(half8_t, read_x(lds0, i, s)), &hi, &lo);
+        for (int j = 0; j < NT; ++j) wv[j] = mx_frag_bf16(far, w[0][j][s], ws[0][j]);
+#pragma unroll
+        for (int i = 0; i < MS; ++i) {
+          half8_t hi = __builtin_bit_cast(half8_t, read_x(lds0, i, s)), lo;
+          if (!BF16) split_f16(hi, &hi, &lo);
+#pragma unroll 1
+          for (int times = far ? 4 : 1; times > 0; --times)
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
               acc[i][j] = mfma(__builtin_bit_cast(u32x4_t, hi), wv[j], acc[i][j], std::true_type());
-              acc[i][j] = mfma(__builtin_bit_cast(u32x4_t, lo), wv[j], acc[i][j], std::true_type());
+              if (!BF16) acc[i][j] = mfma(__builtin_bit_cast(u32x4_t, lo), wv[j], acc[i][j], std::true_type());
             }
-          }
         }
       }
     }

@@ -114,18 +114,60 @@ template <bool BF16, int CT> struct MxWeights : MxTiles<CT> {
     this->load_scales(unit, live, r);
     this->load_codes(unit, live, lds, 0, 1);
   }
+  // acc += a . unit by the path of scales outside the type's range: the weights in
+  // bf16, fp16 activations as two bf16 parts
+  template <int MT, int PL, class A>
+  __device__ __forceinline__ void multiply_bf16(const uint8_t* lds, const uint32_t (&b)[CT][4], const A& a, int nmt,
+                                                floatx4_t (&acc)[MT][CT]) const {
+    bool far = false;
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) far = far || mx_far(b[t][j]);
+    far = __any(far);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x4_t c[CT];
+#pragma unroll
+      for (int t = 0; t < CT; ++t) c[t] = this->block(lds, t, j);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        half8_t w[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t) w[t] = mx_frag_bf16(far, c[t][v], b[t][j]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          if (mt >= nmt) break;
+#pragma unroll
+          for (int pl = 0; pl < PL; ++pl) {
+            half8_t hi = a(mt, pl, 4 * j + v), lo;
+            if (!BF16) split_f16(hi, &hi, &lo);
+#pragma unroll 1
+            for (int times = far ? 4 : 1; times > 0; --times)
+#pragma unroll
+              for (int t = 0; t < CT; ++t) {
+                acc[mt][t] = mfma16<true>(hi, w[t], acc[mt][t]);
+                if (!BF16) acc[mt][t] = mfma16<true>(lo, w[t], acc[mt][t]);
+              }
+          }
+        }
+      }
+    }
+  }
   // acc += a . unit, a(mt, pl, step) the rows' eight values
   template <int MT, int PL, class A>
   __device__ __forceinline__ void multiply(const uint8_t* lds, const Regs& r, int unit, const A& a, int nmt,
                                            floatx4_t (&acc)[MT][CT]) const {
     uint32_t b[CT][4];
     bool fits = true;
+    uint32_t top = 0;
 #pragma unroll
     for (int t = 0; t < CT; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         b[t][j] = this->byte_of(r, t, j, unit);
-        fits = fits && mx_fits_f16(b[t][j]);
+        if (BF16) top = max(top, b[t][j]);
+        else fits = fits && mx_fits_f16(b[t][j]);
       }
     if (!BF16 && !__all(fits)) {                   // ordinary weights do not come here
       fits = true;
@@ -134,33 +176,13 @@ template <bool BF16, int CT> struct MxWeights : MxTiles<CT> {
 #pragma unroll
         for (int j = 0; j < 4; ++j) fits = fits && (mx_fits_f16(b[t][j]) || mx_zero(this->block(lds, t, j)));
     }
-    if (!BF16 && !__all(fits)) {
-      // a scale outside fp16's range: the block in bf16 (which holds every
-      // MXFP4 value), the activations as two bf16 parts
+    if (!BF16 && !__all(fits)) return multiply_bf16<MT, PL>(lds, b, a, nmt, acc);
+    floatx4_t before[MT][CT];                      // bf16: the sums, should a byte be above 252
+    if constexpr (BF16) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u32x4_t c[CT];
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int t = 0; t < CT; ++t) c[t] = this->block(lds, t, j);
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if (mt >= nmt) break;
-#pragma unroll
-            for (int pl = 0; pl < PL; ++pl) {
-              half8_t hi, lo;
-              split_f16(a(mt, pl, 4 * j + v), &hi, &lo);
-#pragma unroll
-              for (int t = 0; t < CT; ++t) {
-                const half8_t w = mx_frag<true>(c[t][v], mx_scale(b[t][j]));
-                acc[mt][t] = mfma16<true>(hi, w, acc[mt][t]);
-                acc[mt][t] = mfma16<true>(lo, w, acc[mt][t]);
-              }
-            }
-          }
-      }
-      return;
+        for (int t = 0; t < CT; ++t) before[mt][t] = acc[mt][t];
     }
     // four steps' operands are read at once, the next four while these multiply:
     // an LDS read per step leaves its latency in every step
@@ -190,7 +212,8 @@ template <bool BF16, int CT> struct MxWeights : MxTiles<CT> {
       for (int v = 0; v < 4; ++v) {
         half8_t w[CT];
 #pragma unroll
-        for (int t = 0; t < CT; ++t) w[t] = mx_frag<BF16>(c[d][t][v], mx_scale(b[t][j]));
+        for (int t = 0; t < CT; ++t)
+          w[t] = mx_frag<BF16>(c[d][t][v], mx_scale(b[t][j]));
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           if (mt >= nmt) break;
@@ -201,6 +224,16 @@ template <bool BF16, int CT> struct MxWeights : MxTiles<CT> {
         }
       }
       __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (BF16) {
+      if (__any(top > kMxExact)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int t = 0; t < CT; ++t) acc[mt][t] = before[mt][t];
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);   // nothing stays in registers for it
+        multiply_bf16<MT, PL>(lds, b, a, nmt, acc);
+      }
     }
   }
 };
