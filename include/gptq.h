@@ -431,6 +431,13 @@ GPTQ_API int gptq_mxfp4_quantize(const void* x, int x_type, int64_t M, int64_t K
 GPTQ_API int gptq_mxfp4_quantize_check(const void* x, int x_type, int64_t M, int64_t K, const uint8_t* codes,
                                        const uint8_t* scales);
 
+/* Kernel and launch shape of a quantisation of [M, K], and of a product (host
+ * only), as gptq_gemm_describe. */
+GPTQ_API int gptq_mxfp4_quantize_describe(int x_type, int64_t M, int64_t K, char* buf, int64_t buflen);
+GPTQ_API int gptq_mxfp4_gemm_describe(const void* x, int x_type, const uint8_t* x_scales, const uint8_t* codes,
+                                      const uint8_t* scales, int64_t M, int64_t N, int64_t K, const void* out,
+                                      int out_type, char* buf, int64_t buflen);
+
 /* MXFP4 -> values [M, K] in out_type (fp16, bf16 or fp32), rounded once to
  * nearest even: exact in bf16 and fp32 for scale bytes up to 252 (values of 2^128
  * and above, under bytes 253 and 254, become infinities), in fp16 for 104 .. 140. */

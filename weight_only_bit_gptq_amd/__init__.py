@@ -122,10 +122,12 @@ def library() -> ctypes.CDLL:
         lib.gptq_mxfp4_dequant.argtypes = [vp, vp, i64, i64, vp, i32, vp]
         lib.gptq_mxfp4_gemm.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, vp, i32, vp]
         lib.gptq_mxfp4_gemm_check.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, vp, i32]
+        lib.gptq_mxfp4_quantize_describe.argtypes = [i32, i64, i64, ctypes.c_char_p, i64]
+        lib.gptq_mxfp4_gemm_describe.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, vp, i32, ctypes.c_char_p, i64]
         pex = ctypes.POINTER(ExpertStack)
         lib.gptq_moe_layer.argtypes = [vp, i32, vp, i64, i64, i64, i64, i64, i32, pex, pex, vp, vp]
         lib.gptq_moe_layer_check.argtypes = [vp, i32, vp, i64, i64, i64, i64, i64, i32, pex, pex, vp]
-        for name in ("quantize", "quantize_check", "dequant", "gemm", "gemm_check"):
+        for name in ("quantize", "quantize_check", "quantize_describe", "dequant", "gemm", "gemm_check", "gemm_describe"):
             getattr(lib, "gptq_mxfp4_" + name).restype = i32
         lib.gptq_moe_layer.restype = lib.gptq_moe_layer_check.restype = i32
         lib.gptq_strerror.argtypes = [i32]

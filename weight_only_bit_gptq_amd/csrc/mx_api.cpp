@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdio>
 #include <new>
 
 #include "gptq.h"
@@ -67,6 +68,22 @@ gptq::ExpertStack stack_of(const gptq_experts* s, int64_t rows, int64_t cols) {
   return e;
 }
 
+gptq::MxGemmArgs args_of(const void* x, int x_type, const uint8_t* x_scales, const uint8_t* codes,
+                         const uint8_t* scales, int64_t M, int64_t N, int64_t K, void* out, int out_type) {
+  gptq::MxGemmArgs a{};
+  a.x = x;
+  a.x_scales = x_scales;
+  a.codes = codes;
+  a.scales = scales;
+  a.out = out;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.x_type = x_type;
+  a.out_type = out_type;
+  return a;
+}
+
 int status_of(hipError_t err) { return err == hipSuccess ? GPTQ_OK : GPTQ_ERR_LAUNCH; }
 
 }  // namespace
@@ -107,21 +124,41 @@ int gptq_mxfp4_gemm_check(const void* x, int x_type, const uint8_t* x_scales, co
   return GPTQ_OK;
 }
 
+int gptq_mxfp4_quantize_describe(int x_type, int64_t M, int64_t K, char* buf, int64_t buflen) {
+  if (!buf || buflen <= 0) return GPTQ_ERR_NULL_PTR;
+  buf[0] = '\0';
+  if (x_type < GPTQ_TYPE_F16 || x_type > GPTQ_TYPE_F32) return GPTQ_ERR_BAD_ARG;
+  const int rc = check_mx(nullptr, nullptr, nullptr, 0, K);
+  if (rc != GPTQ_OK || M < 0 || M >= kMaxElems) return GPTQ_ERR_BAD_SHAPE;
+  if (M == 0) std::snprintf(buf, (size_t)buflen, "none (M = 0)");
+  else gptq::describe_mx_quantize(x_type, M, K, buf, (size_t)buflen);
+  return GPTQ_OK;
+}
+
+int gptq_mxfp4_gemm_describe(const void* x, int x_type, const uint8_t* x_scales, const uint8_t* codes,
+                             const uint8_t* scales, int64_t M, int64_t N, int64_t K, const void* out, int out_type,
+                             char* buf, int64_t buflen) {
+  if (!buf || buflen <= 0) return GPTQ_ERR_NULL_PTR;
+  buf[0] = '\0';
+  const int rc = gptq_mxfp4_gemm_check(x, x_type, x_scales, codes, scales, M, N, K, out, out_type);
+  if (rc != GPTQ_OK) return rc;
+  if (M == 0) {
+    std::snprintf(buf, (size_t)buflen, "none (M = 0)");
+  } else {
+    gptq::MxGemmArgs a = args_of(x, x_type, x_scales, codes, scales, M, N, K, const_cast<void*>(out), out_type);
+    size_t counters = 0;
+    gptq::plan_mx_gemm(&a, true, &counters);
+    const gptq::MxKernel k = gptq::mx_gemm_kernel(a);
+    std::snprintf(buf, (size_t)buflen, "%s grid=%u block=%u k_splits=%d", k.name, k.grid, k.block, a.splits);
+  }
+  return GPTQ_OK;
+}
+
 int gptq_mxfp4_gemm(const void* x, int x_type, const uint8_t* x_scales, const uint8_t* codes, const uint8_t* scales,
                     int64_t M, int64_t N, int64_t K, void* out, int out_type, void* stream) {
   const int rc = gptq_mxfp4_gemm_check(x, x_type, x_scales, codes, scales, M, N, K, out, out_type);
   if (rc != GPTQ_OK || M == 0) return rc;
-  gptq::MxGemmArgs a{};
-  a.x = x;
-  a.x_scales = x_scales;
-  a.codes = codes;
-  a.scales = scales;
-  a.out = out;
-  a.M = (int)M;
-  a.N = (int)N;
-  a.K = (int)K;
-  a.x_type = x_type;
-  a.out_type = out_type;
+  gptq::MxGemmArgs a = args_of(x, x_type, x_scales, codes, scales, M, N, K, out, out_type);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   try {
     size_t counters = 0;

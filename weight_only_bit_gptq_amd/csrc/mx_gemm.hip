@@ -231,25 +231,16 @@ size_t lds_of(const MxGemmArgs& a) {
   return a.M <= 16 ? stream_lds<1, 1>(a) : a.M <= 32 ? stream_lds<2, 1>(a) : stream_lds<4, 1>(a);
 }
 
-template <int MT, int CT> hipError_t stream_typed(const MxGemmArgs& a, hipStream_t stream) {
-  const int cols = 16 * CT * a.nwc, nw = a.nwc * a.nwk;
-  const unsigned grid = (unsigned)((a.N + cols - 1) / cols) * (unsigned)((a.M + 16 * MT - 1) / (16 * MT)) * (unsigned)a.splits;
-  const size_t lds = stream_lds<MT, CT>(a);
-  auto go = [&](auto kernel) {
-    if (lds > 64 * 1024) {
-      const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-      if (err != hipSuccess) return err;
-    }
-    kernel<<<grid, 64 * nw, lds, stream>>>(a);
-    return hipGetLastError();
-  };
-  if (a.x_type == kTypeMxfp4) return go(mx4_stream_kernel<MT, CT>);
+// (16-bit x has at most 32 rows here: MT <= 2)
+template <int MT, int CT> MxKernel stream_kernel_of(const MxGemmArgs& a, const char* const (&names)[3]) {
+  const int cols = 16 * CT * a.nwc;
+  MxKernel k{mx4_stream_kernel<MT, CT>, names[0], 0, 64u * (unsigned)(a.nwc * a.nwk), stream_lds<MT, CT>(a)};
+  k.grid = (unsigned)((a.N + cols - 1) / cols) * (unsigned)((a.M + 16 * MT - 1) / (16 * MT)) * (unsigned)a.splits;
   if constexpr (MT <= 2) {
-    if (a.x_type == kTypeBf16) return go(mx_stream_kernel<true, MT, CT>);
-    return go(mx_stream_kernel<false, MT, CT>);
+    if (a.x_type == kTypeBf16) k.fn = mx_stream_kernel<true, MT, CT>, k.name = names[1];
+    else if (a.x_type == kTypeF16) k.fn = mx_stream_kernel<false, MT, CT>, k.name = names[2];
   }
-  return hipErrorInvalidValue;                     // not planned
+  return k;
 }
 
 size_t plan_mx_gemm(MxGemmArgs* a, bool allow_split, size_t* counter_bytes) {
@@ -324,11 +315,29 @@ size_t plan_mx_gemm(MxGemmArgs* a, bool allow_split, size_t* counter_bytes) {
   return a->splits > 1 ? (size_t)a->splits * (size_t)a->M * (size_t)a->N * 4 : 0;
 }
 
+MxKernel mx_gemm_kernel(const MxGemmArgs& a) {
+  if (a.tile_m != 0) return mx_tile_kernel_of(a);
+  if (a.M <= 16)
+    return stream_kernel_of<1, 1>(a, {"gptq::mx4_stream_kernel<1, 1>", "gptq::mx_stream_kernel<true, 1, 1>",
+                                      "gptq::mx_stream_kernel<false, 1, 1>"});
+  if (a.M <= 32)
+    return stream_kernel_of<2, 1>(a, {"gptq::mx4_stream_kernel<2, 1>", "gptq::mx_stream_kernel<true, 2, 1>",
+                                      "gptq::mx_stream_kernel<false, 2, 1>"});
+  return stream_kernel_of<4, 1>(a, {"gptq::mx4_stream_kernel<4, 1>", "", ""});
+}
+
+hipError_t launch_mx_kernel(const MxKernel& k, const MxGemmArgs& a, hipStream_t stream) {
+  if (k.lds > 64 * 1024) {
+    const hipError_t err =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(k.fn), hipFuncAttributeMaxDynamicSharedMemorySize, (int)k.lds);
+    if (err != hipSuccess) return err;
+  }
+  k.fn<<<k.grid, k.block, k.lds, stream>>>(a);
+  return hipGetLastError();
+}
+
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
-  if (a.tile_m != 0) return launch_mx_tile(a, stream);
-  if (a.M <= 16) return stream_typed<1, 1>(a, stream);
-  if (a.M <= 32) return stream_typed<2, 1>(a, stream);
-  return stream_typed<4, 1>(a, stream);
+  return a.tile_m != 0 ? launch_mx_tile(a, stream) : launch_mx_kernel(mx_gemm_kernel(a), a, stream);
 }
 
 }  // namespace gptq

@@ -12,6 +12,9 @@ hipError_t launch_mx_quantize(const void* x, int type, int64_t M, int64_t K, uin
 hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out, int type,
                              hipStream_t stream);
 
+// Kernel and launch shape of a quantisation, as text.
+void describe_mx_quantize(int type, int64_t M, int64_t K, char* buf, size_t n);
+
 struct MxGemmArgs {
   const void* x;             // [M, K] fp16 / bf16, or MXFP4 codes [M, K/2]
   const uint8_t* x_scales;   // [M, K/32] (MXFP4 activations)
@@ -37,6 +40,16 @@ struct MxGemmArgs {
 size_t plan_mx_gemm(MxGemmArgs* a, bool allow_split, size_t* counter_bytes);
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
 hipError_t launch_mx_tile(const MxGemmArgs& a, hipStream_t stream);
+// A planned product's kernel: what is launched, its name, grid and LDS.
+struct MxKernel {
+  void (*fn)(MxGemmArgs);
+  const char* name;
+  unsigned grid, block;
+  size_t lds;                // dynamic
+};
+MxKernel mx_gemm_kernel(const MxGemmArgs& a);
+MxKernel mx_tile_kernel_of(const MxGemmArgs& a);
+hipError_t launch_mx_kernel(const MxKernel& k, const MxGemmArgs& a, hipStream_t stream);
 
 // One stack of expert weights, [rows -> cols] per expert.
 struct ExpertStack {

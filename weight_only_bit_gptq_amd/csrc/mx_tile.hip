@@ -458,33 +458,30 @@ __global__ __launch_bounds__(256) void mx_split_sum_kernel(MxGemmArgs a) {
   }
 }
 
-hipError_t launch_mx_tile(const MxGemmArgs& a, hipStream_t stream) {
+#define MX_KERNEL(...) MxKernel{__VA_ARGS__, "gptq::" #__VA_ARGS__, grid, 256, 0}
+MxKernel mx_tile_kernel_of(const MxGemmArgs& a) {
   const int nt = a.tiles_m * a.tiles_n;
   const unsigned grid = (unsigned)(8 * ((nt + 7) / 8) * a.splits);
+  if (a.x_type != kTypeMxfp4) {
+    if (a.x_type == kTypeBf16) return a.tile_m == 128 ? MX_KERNEL(mx_tile_kernel<true, 128>) : MX_KERNEL(mx_tile_kernel<true, 64>);
+    return a.tile_m == 128 ? MX_KERNEL(mx_tile_kernel<false, 128>) : MX_KERNEL(mx_tile_kernel<false, 64>);
+  }
   const bool aligned = (a.K / 32) % 4 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0 &&
                        (reinterpret_cast<uintptr_t>(a.x_scales) & 3) == 0;
-  auto go4 = [&](auto kernel, int rows, int stages) {
-    const int lds = stages * rows * (128 + 8);
-    hipError_t err = hipSuccess;
-    if (lds > 64 * 1024)
-      err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (err != hipSuccess) return err;
-    kernel<<<grid, 256, lds, stream>>>(a);
-    return hipGetLastError();
+  auto staged = [](MxKernel k, int rows, int stages) {
+    k.lds = (size_t)stages * rows * (128 + 8);
+    return k;
   };
-  hipError_t err;
-  if (a.x_type == kTypeMxfp4) {
-    if (a.tile_m == 256) err = aligned ? go4(mx4_tile_kernel<4, 2, true>, 512, 2) : go4(mx4_tile_kernel<4, 2, false>, 512, 2);
-    else if (!aligned) err = go4(mx4_tile_kernel<2, 2, false>, 256, 2);
-    else if (nt * a.splits <= 256) err = go4(mx4_tile_kernel<2, 4, true>, 256, 4);
-    else err = go4(mx4_tile_kernel<2, 2, true>, 256, 2);
-  } else {
-    if (a.x_type == kTypeBf16 && a.tile_m == 128) mx_tile_kernel<true, 128><<<grid, 256, 0, stream>>>(a);
-    else if (a.x_type == kTypeBf16) mx_tile_kernel<true, 64><<<grid, 256, 0, stream>>>(a);
-    else if (a.tile_m == 128) mx_tile_kernel<false, 128><<<grid, 256, 0, stream>>>(a);
-    else mx_tile_kernel<false, 64><<<grid, 256, 0, stream>>>(a);
-    err = hipGetLastError();
-  }
+  if (a.tile_m == 256)
+    return staged(aligned ? MX_KERNEL(mx4_tile_kernel<4, 2, true>) : MX_KERNEL(mx4_tile_kernel<4, 2, false>), 512, 2);
+  if (!aligned) return staged(MX_KERNEL(mx4_tile_kernel<2, 2, false>), 256, 2);
+  if (nt * a.splits <= 256) return staged(MX_KERNEL(mx4_tile_kernel<2, 4, true>), 256, 4);
+  return staged(MX_KERNEL(mx4_tile_kernel<2, 2, true>), 256, 2);
+}
+#undef MX_KERNEL
+
+hipError_t launch_mx_tile(const MxGemmArgs& a, hipStream_t stream) {
+  hipError_t err = launch_mx_kernel(mx_tile_kernel_of(a), a, stream);
   if (err == hipSuccess && a.splits > 1) {
     const int64_t quads = ((int64_t)a.M * a.N + 3) / 4;
     mx_split_sum_kernel<<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(a);

@@ -11,6 +11,7 @@
 // join them.  Measured, 28672 x 8192: bf16 92 us quantise (6.4 TB/s), 84 us back
 // (7.1); fp32 173 us quantise, 148 us back (7.2).
 #include <algorithm>
+#include <cstdio>
 
 #include "mx_device.hpp"
 #include "mx_kernels.hpp"
@@ -153,6 +154,14 @@ hipError_t dequant_typed(const uint8_t* codes, const uint8_t* scales, int64_t pi
     if (err != hipSuccess) return err;
   }
   return hipSuccess;
+}
+
+void describe_mx_quantize(int type, int64_t M, int64_t K, char* buf, size_t n) {
+  const int64_t pieces = M * K / (type == kTypeF32 ? 4 : 8), one = std::min(pieces, kMxLaunchPieces);
+  const int per = one >= kMxWideFrom ? kMxPieces : 1;
+  std::snprintf(buf, n, "gptq::mx_quantize_kernel<%d, %d> grid=%lld block=256 launches=%lld", type, per,
+                       (long long)((one + 256 * per - 1) / (256 * per)),
+                       (long long)((pieces + kMxLaunchPieces - 1) / kMxLaunchPieces));
 }
 
 hipError_t launch_mx_quantize(const void* x, int type, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales,
