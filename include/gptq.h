@@ -30,8 +30,9 @@
  * stream) and is asynchronous: buffers must stay valid until that work
  * completes, and a device-side fault surfaces at the caller's next
  * synchronisation.  The library's own device memory: a workspace per
- * (device, stream) -- split-K partial sums and arrival counters, and the
- * gathered x of gptq_gemm_sorted -- allocated (hipMalloc, zeroed on the
+ * (device, stream) -- split-K partial sums and arrival counters, the gathered
+ * x of gptq_gemm_sorted, the choices and hidden values of gptq_moe_layer --
+ * allocated (hipMalloc, zeroed on the
  * stream) by the first call on that stream that needs it, and replaced by a
  * larger one when a later call needs more; a replaced buffer is not freed
  * until gptq_release, because work queued earlier and graphs captured earlier
@@ -39,7 +40,7 @@
  * temporary freed on the same stream.
  * HIP graphs: calls on one stream may be captured.  A capture never allocates
  * (a split-K call captured before its stream has a workspace runs unsplit
- * instead; gptq_gemm_sorted returns GPTQ_ERR_NO_MEM), and the graph keeps
+ * instead; gptq_gemm_sorted and gptq_moe_layer return GPTQ_ERR_NO_MEM), and the graph keeps
  * using the workspace its capture stream had at capture time.  So a replay
  * shares that workspace with every other call on the capture stream: replays
  * (on any stream) must not overlap such calls or each other, and
