@@ -340,7 +340,7 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cw = wave % g.nwc, kw = wave / g.nwc;
   const int tile = (int)blockIdx.x % tiles, sb = (int)blockIdx.x / tiles;
-  const int slot = sb / g.row_blocks, rb = sb % g.row_blocks;
+  const int slot = sb / a.row_blocks, rb = sb % a.row_blocks;
   const int n0 = tile * cols + 16 * CS * cw;
   const bool by_pair = pairs < a.E;
   const int e = by_pair ? __builtin_amdgcn_readfirstlane(a.chosen[slot]) : slot;
@@ -624,7 +624,7 @@ __global__ __launch_bounds__(512, 2) void moe_down_kernel(MoeArgs a) {
 
   // this workgroup's units [f0, f1) of all experts' units in a row
   const int total = experts * units;
-  const int f0 = (int)((int64_t)total * split / g.splits), f1 = (int)((int64_t)total * (split + 1) / g.splits);
+  const int f0 = (int)((int64_t)total * split / a.splits), f1 = (int)((int64_t)total * (split + 1) / a.splits);
   struct Phase {
     int slot, rb, unit;              // first unit of the phase within the expert
     int end;                         // the workgroup's last unit of the expert
@@ -735,15 +735,15 @@ __global__ __launch_bounds__(512, 2) void moe_down_kernel(MoeArgs a) {
     float s = all[i];
     for (int k = 1; k < g.nwk; ++k) s += all[k * a.T * cols + i];
     const int64_t o = (int64_t)(i / cols) * a.H + n;
-    if (g.splits > 1) put_agent(a.part + (int64_t)split * a.T * a.H + o, s);
+    if (a.splits > 1) put_agent(a.part + (int64_t)split * a.T * a.H + o, s);
     else store_typed(a.out, o, s, a.bf16 ? kTypeBf16 : kTypeF16);
   }
-  if (g.splits == 1 || !last_arrival(a.cnt + tile, (uint32_t)g.splits, &flag)) return;
+  if (a.splits == 1 || !last_arrival(a.cnt + tile, (uint32_t)a.splits, &flag)) return;
   for (int i = tid; i < a.T * cols; i += blockDim.x) {
     const int n = tile * cols + i % cols;
     if (n >= a.H) continue;
     const int64_t o = (int64_t)(i / cols) * a.H + n;
-    store_typed(a.out, o, sum_splits<kMoeMaxSplits>(a.part + o, (int64_t)a.T * a.H, g.splits),
+    store_typed(a.out, o, sum_splits<kMoeMaxSplits>(a.part + o, (int64_t)a.T * a.H, a.splits),
                 a.bf16 ? kTypeBf16 : kTypeF16);
   }
 }
@@ -792,9 +792,7 @@ size_t plan_moe(MoeArgs* a, char* base, size_t* counter_bytes) {
   while (block < 32 && (size_t)block * a->E < 2 * P) block *= 2;
   u.block_rows = std::min(a->T, block);
   d.block_rows = std::min(u.block_rows, 16);
-  u.row_blocks = (a->T + u.block_rows - 1) / u.block_rows;
-  d.row_blocks = 1;
-  u.splits = 1;
+  a->row_blocks = (a->T + u.block_rows - 1) / u.block_rows;
   // Column waves share the staged rows, k waves (at least as many as make up
   // x's chunks of 512 k) need fewer column tiles.  Eight waves (four where a
   // wave's registers leave two per SIMD); fewer columns and more k while the
@@ -826,7 +824,7 @@ size_t plan_moe(MoeArgs* a, char* base, size_t* counter_bytes) {
   const int tiles = (a->H + dc * d.nwc - 1) / (dc * d.nwc);
   const int units = slots * ((a->I + kd - 1) / kd);
   const int fit = down_lds(*a) + 13 * 1024 <= 80 * 1024 ? 2 : 1;
-  d.splits = std::max(1, std::min({fit * kMoeCUs / tiles, units / d.nwk, kMoeMaxSplits}));
+  a->splits = std::max(1, std::min({fit * kMoeCUs / tiles, units / d.nwk, kMoeMaxSplits}));
   *counter_bytes = (size_t)tiles * 4;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -842,7 +840,7 @@ size_t plan_moe(MoeArgs* a, char* base, size_t* counter_bytes) {
   const bool fp16_parts = !a->bf16 && a->down.bits != 0;
   a->split_first = fp16_parts && d.block_rows > kWideRows;
   a->split_h = reinterpret_cast<uint16_t*>(take(a->split_first ? P * (size_t)a->I * 4 : 0));
-  a->part = reinterpret_cast<float*>(take(d.splits > 1 ? (size_t)d.splits * T * (size_t)a->H * 4 : 0));
+  a->part = reinterpret_cast<float*>(take(a->splits > 1 ? (size_t)a->splits * T * (size_t)a->H * 4 : 0));
   return off;
 }
 
@@ -864,7 +862,7 @@ hipError_t gate_up_typed(const MoeArgs& a, hipStream_t stream) {
   constexpr int CS = segment_tiles(FMT, TILED);
   const MoeShape& g = a.up_shape;
   const int cols = 16 * CS * g.nwc;
-  const unsigned grid = (unsigned)(std::min(a.E, a.T * a.k) * g.row_blocks * ((a.I + cols - 1) / cols));
+  const unsigned grid = (unsigned)(std::min(a.E, a.T * a.k) * a.row_blocks * ((a.I + cols - 1) / cols));
   const size_t lds = up_lds(a);
   const int unit = unit_of(a.gate_up, 2);
   if (FMT == 0 || a.gate_up.group_size % 128 == 0)
@@ -878,7 +876,7 @@ template <int FMT, bool TILED, bool BF16, bool WIDE> hipError_t down_typed(const
   constexpr int CS = segment_tiles(FMT, TILED);
   const MoeShape& g = a.down_shape;
   const int cols = 16 * CS * g.nwc;
-  const unsigned grid = (unsigned)(g.splits * ((a.H + cols - 1) / cols));
+  const unsigned grid = (unsigned)(a.splits * ((a.H + cols - 1) / cols));
   const size_t lds = down_lds(a);
   const int unit = unit_of(a.down, 1);
   if (FMT == 0 || a.down.group_size % 128 == 0)

@@ -17,7 +17,7 @@ constexpr int kStreamSplits = 8;                   // workgroups along K per til
 // to arrive.  red: nwc nwk MT CT x 1 KB.
 template <int MT, int CT>
 __device__ __forceinline__ void finish_stream(const MxGemmArgs& a, const floatx4_t (&acc)[MT][CT], floatx4_t* red, int* flag,
-                                              int m0, int n0, int rows, int nmt, int split, int tile) {
+                                              int n0, int nmt, int split, int tile) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cw = wave % a.nwc, kw = wave / a.nwc;
   if (a.nwk > 1) {
@@ -45,8 +45,8 @@ __device__ __forceinline__ void finish_stream(const MxGemmArgs& a, const floatx4
       const int m = 16 * mt + 4 * (lane >> 4), n = n0 + (cw * CT + j) * 16 + (lane & 15);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (m + i >= rows || n >= a.N) continue;
-        const int64_t o = (int64_t)(m0 + m + i) * a.N + n;
+        if (m + i >= a.M || n >= a.N) continue;
+        const int64_t o = (int64_t)(m + i) * a.N + n;
         if (a.splits > 1) put_agent(a.ws + (int64_t)split * a.M * a.N + o, s[i]);
         else store_typed(a.out, o, s[i], a.out_type);
       }
@@ -54,22 +54,22 @@ __device__ __forceinline__ void finish_stream(const MxGemmArgs& a, const floatx4
   }
   if (a.splits == 1 || !last_arrival(a.cnt + tile, (uint32_t)a.splits, flag)) return;
   const int cols = 16 * CT * a.nwc;
-  for (int i = threadIdx.x; i < rows * cols; i += blockDim.x) {
+  for (int i = threadIdx.x; i < a.M * cols; i += blockDim.x) {
     const int n = n0 + i % cols;
     if (n >= a.N) continue;
-    const int64_t o = (int64_t)(m0 + i / cols) * a.N + n;
+    const int64_t o = (int64_t)(i / cols) * a.N + n;
     store_typed(a.out, o, sum_splits<kStreamSplits>(a.ws + o, (int64_t)a.M * a.N, a.splits), a.out_type);
   }
 }
 
-// Workgroup -> (split, row block, column tile)
+// Workgroup -> (split, column tile); every workgroup has all rows, at most 16 MT.
 struct StreamPlace {
-  int split, tile, m0, n0;
+  int split, tile, n0;
 };
-template <int MT, int CT> __device__ __forceinline__ StreamPlace place_of(const MxGemmArgs& a) {
-  const int cols = 16 * CT * a.nwc, tn = (a.N + cols - 1) / cols, tm = (a.M + 16 * MT - 1) / (16 * MT);
-  const int b = (int)blockIdx.x, split = b / (tn * tm), tile = b - split * tn * tm;
-  return StreamPlace{split, tile, tile / tn * 16 * MT, tile % tn * cols};
+template <int CT> __device__ __forceinline__ StreamPlace place_of(const MxGemmArgs& a) {
+  const int cols = 16 * CT * a.nwc, tiles = (a.N + cols - 1) / cols;
+  const int b = (int)blockIdx.x, split = b / tiles, tile = b - split * tiles;
+  return StreamPlace{split, tile, tile * cols};
 }
 
 // LDS of one phase: nwk k waves' units of x and every wave's units of weights.
@@ -82,8 +82,8 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void mx_stream_kernel(MxGemmA
   const int lane = threadIdx.x & 63, nw = a.nwc * a.nwk;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cw = wave % a.nwc, kw = wave / a.nwc;
-  const StreamPlace at = place_of<MT, CT>(a);
-  const int rows = min(16 * MT, a.M - at.m0), nmt = (rows + 15) >> 4;
+  const StreamPlace at = place_of<CT>(a);
+  const int rows = a.M, nmt = (rows + 15) >> 4;
   W w;
   w.place(a.K, lane);
   w.bind(a.codes, a.scales, a.N, a.K);
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void mx_stream_kernel(MxGemmA
   auto rows_at = [&](int p) __attribute__((always_inline)) { return lds + (p & 1) * phase; };
   typename W::Regs r0, r1;
   w.load(ua + kw, ua + kw < ub, weights(0), &r0);
-  if (threadIdx.x < rows) off[threadIdx.x] = (uint32_t)(at.m0 + threadIdx.x) * (uint32_t)a.K * 2u;
+  if (threadIdx.x < rows) off[threadIdx.x] = threadIdx.x * (uint32_t)a.K * 2u;
   __syncthreads();
   floatx4_t acc[MT][CT];
 #pragma unroll
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void mx_stream_kernel(MxGemmA
     if (p + 2 < phases) issue(p + 2, &r0);
     compute(p + 1, r1);
   }
-  finish_stream<MT, CT>(a, acc, reinterpret_cast<floatx4_t*>(lds), &flag, at.m0, at.n0, rows, nmt, at.split, at.tile);
+  finish_stream<MT, CT>(a, acc, reinterpret_cast<floatx4_t*>(lds), &flag, at.n0, nmt, at.split, at.tile);
 }
 
 // MXFP4 activations: both operands' blocks as they are; lane l holds row l % 16
@@ -150,13 +150,13 @@ __global__ __launch_bounds__(512, 2) void mx4_stream_kernel(MxGemmArgs a) {
   const int lane = threadIdx.x & 63, nw = a.nwc * a.nwk;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cw = wave % a.nwc, kw = wave / a.nwc;
-  const StreamPlace at = place_of<MT, CT>(a);
-  const int rows = min(16 * MT, a.M - at.m0), nmt = (rows + 15) >> 4;
+  const StreamPlace at = place_of<CT>(a);
+  const int nmt = (a.M + 15) >> 4;
   X x;
   x.place(a.K, lane);
   x.bind(static_cast<const uint8_t*>(a.x), a.x_scales, a.M, a.K);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) x.row0[mt] = (uint32_t)(at.m0 + 16 * mt);
+  for (int mt = 0; mt < MT; ++mt) x.row0[mt] = 16u * (uint32_t)mt;
   W w;
   w.place(a.K, lane);
   w.bind(a.codes, a.scales, a.N, a.K);
@@ -215,13 +215,13 @@ __global__ __launch_bounds__(512, 2) void mx4_stream_kernel(MxGemmArgs a) {
     if (p + 2 < phases) issue(p + 2, &x0, &w0);
     compute(p + 1, x1, w1);
   }
-  finish_stream<MT, CT>(a, acc, reinterpret_cast<floatx4_t*>(lds), &flag, at.m0, at.n0, rows, nmt, at.split, at.tile);
+  finish_stream<MT, CT>(a, acc, reinterpret_cast<floatx4_t*>(lds), &flag, at.n0, nmt, at.split, at.tile);
 }
 
 // Dynamic LDS of a launch: two phases, or the k waves' sums.
 template <int MT, int CT> size_t stream_lds(const MxGemmArgs& a) {
   const size_t nw = (size_t)a.nwc * a.nwk, sums = a.nwk > 1 ? nw * MT * CT * 1024 : 0;
-  const size_t x = a.x_type == kTypeMxfp4 ? (size_t)a.nwk * MT * 4096 : (size_t)std::min(a.M, 16 * MT) * a.nwk * 1024;
+  const size_t x = a.x_type == kTypeMxfp4 ? (size_t)a.nwk * MT * 4096 : (size_t)a.M * a.nwk * 1024;
   return std::max(sums, 2 * (x + nw * CT * 4096));
 }
 
@@ -235,10 +235,12 @@ size_t lds_of(const MxGemmArgs& a) {
 template <int MT, int CT> MxKernel stream_kernel_of(const MxGemmArgs& a, const char* const (&names)[3]) {
   const int cols = 16 * CT * a.nwc;
   MxKernel k{mx4_stream_kernel<MT, CT>, names[0], 0, 64u * (unsigned)(a.nwc * a.nwk), stream_lds<MT, CT>(a)};
-  k.grid = (unsigned)((a.N + cols - 1) / cols) * (unsigned)((a.M + 16 * MT - 1) / (16 * MT)) * (unsigned)a.splits;
+  k.grid = (unsigned)((a.N + cols - 1) / cols) * (unsigned)a.splits;
   if constexpr (MT <= 2) {
     if (a.x_type == kTypeBf16) k.fn = mx_stream_kernel<true, MT, CT>, k.name = names[1];
     else if (a.x_type == kTypeF16) k.fn = mx_stream_kernel<false, MT, CT>, k.name = names[2];
+  } else if (a.x_type != kTypeMxfp4) {
+    k.fn = nullptr;                                // not planned
   }
   return k;
 }
@@ -275,7 +277,7 @@ size_t plan_mx_gemm(MxGemmArgs* a, bool allow_split, size_t* counter_bytes) {
     a->split_tiles = (units + splits - 1) / splits;
     a->splits = (units + a->split_tiles - 1) / a->split_tiles;
     if (a->splits == 1) return 0;
-    *counter_bytes = (size_t)tiles * 4;              // M <= 32 or one row block: a tile per column block
+    *counter_bytes = (size_t)tiles * 4;
     return (size_t)a->splits * (size_t)a->M * (size_t)a->N * 4;
   }
   // Tiles: rows per tile and splits of K by a time model (us) of the measured
@@ -327,6 +329,7 @@ MxKernel mx_gemm_kernel(const MxGemmArgs& a) {
 }
 
 hipError_t launch_mx_kernel(const MxKernel& k, const MxGemmArgs& a, hipStream_t stream) {
+  if (k.fn == nullptr) return hipErrorInvalidValue;
   if (k.lds > 64 * 1024) {
     const hipError_t err =
         hipFuncSetAttribute(reinterpret_cast<const void*>(k.fn), hipFuncAttributeMaxDynamicSharedMemorySize, (int)k.lds);

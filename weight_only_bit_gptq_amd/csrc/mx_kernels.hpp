@@ -62,10 +62,9 @@ struct ExpertStack {
 };
 
 // Launch shape of one of the layer's products: nwc column waves by nwk k waves
-// per workgroup, rows of one expert per row block, row blocks an expert may
-// have, workgroups per column tile.
+// per workgroup, rows of one expert per row block.
 struct MoeShape {
-  int nwc, nwk, block_rows, row_blocks, splits;
+  int nwc, nwk, block_rows;
 };
 
 struct MoeArgs {
@@ -84,9 +83,11 @@ struct MoeArgs {
   int split_first;           // fp32 h goes to split_h [2, T * k, I], two fp16 parts, in
   uint16_t* split_h;         // a kernel of its own; else the down product splits it
   MoeShape up_shape, down_shape;
-  // down product: with several splits per column tile their fp32 sums
+  int row_blocks;            // gate_up: row blocks an expert may have
+  // down product: workgroups per column tile; with several, their fp32 sums
   // [splits, T, H] go to part, the last to arrive (counted in cnt[tile], zero
   // between launches) adds them
+  int splits;
   float* part;
   uint32_t* cnt;
 };

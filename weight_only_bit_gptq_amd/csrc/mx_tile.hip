@@ -211,17 +211,17 @@ __device__ __forceinline__ void mx_tile_body(const MxGemmArgs& a) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
         const int m = m0 + 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
-        if (m < a.M) store((int64_t)m * a.N + n, acc[i][0][v], acc[i][NT - 1][v]);
+        if (m < a.M) store((int64_t)m * a.N + n, acc[i][0][v], acc[i][1][v]);
       }
   };
-  const bool ok0 = n < a.N, ok1 = NT == 2 && n + 1 < a.N;
+  const bool ok0 = n < a.N, ok1 = n + 1 < a.N;
   if (a.splits > 1 || a.out_type == kTypeF32) {
     float* out = a.splits > 1 ? a.ws + (int64_t)sk * a.M * a.N : static_cast<float*>(a.out);
     each([&](int64_t o, float v0, float v1) __attribute__((always_inline)) {
       if (ok0) out[o] = v0;
       if (ok1) out[o + 1] = v1;
     });
-  } else if (NT == 2 && a.pair_stores) {
+  } else if (a.pair_stores) {
     if (!ok0) return;
     uint32_t* out = static_cast<uint32_t*>(a.out);
     if (a.out_type == kTypeBf16)
