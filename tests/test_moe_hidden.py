@@ -119,3 +119,30 @@ def test_zero_nan_and_infinite_fp16_tokens_stay_in_their_row(dev, T):
     assert (np.abs(z.double().cpu().numpy() - ref)[good] <= bound[good]).all()
     assert (z[1] == 0).all() and torch.isnan(z[2]).all() and not torch.isfinite(z[5]).any()
     assert torch.equal(z.isnan(), gq.moe_layer(x, wr, k, s1, s2).isnan())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [4, 5, 64, 66, 70, 130])
+@pytest.mark.parametrize("bits,tiled", [(4, True), (8, False)])
+def test_token_counts_around_the_ways_h_is_split(dev, T, bits, tiled):
+    """Up to four tokens, more, several launches, and a last launch of either kind."""
+    y, ref, bound, _, (x, wr, k, s1, s2) = layer(dev, T, 128, 96, 6, 3, bits, tiled, "fp16", 0.25, 2.0, False, seed=T)
+    assert_within(y, ref, bound)
+    assert torch.equal(gq.moe_layer(x, wr, k, s1, s2, renormalize=False), gq.moe_layer(x, wr, k, s1, s2, renormalize=False))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 20])
+def test_mxfp4_gate_up_before_fp16_gptq_down(dev, T):
+    H, I, E, k = 256, 96, 8, 2
+    rng = np.random.default_rng(T)
+    xt, x = exact_in(rng.standard_normal((T, H)) * 2.0 ** -5, "fp16")
+    wt, wr = exact_in(rng.standard_normal((E, H)) / np.sqrt(H), "fp16")
+    codes, scales = mx_ref.quantize(rng.standard_normal((E, 2 * I, H)) * 0.1)
+    codes.reshape(E, 2 * I, H // 32, 16)[:, ::5, 1] = 0           # blocks of zeros, scale byte 0
+    scales[:, ::5, 1] = 0
+    a2, w2 = stack(rng, E, I, H, 3, 32, True, "fp16", 64.0)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+    y = gq.moe_layer(xt.to(dev), wt.to(dev), k, gq.MxExperts(t(codes), t(scales)), experts(a2, dev))
+    ref, bound = mx_ref.moe_layer(x, wr, k, mx_ref.values(codes, scales), w2, True, torch.finfo(y.dtype).eps)
+    assert_within(y.double().cpu().numpy(), ref, bound + 2.0 ** -25)
