@@ -782,8 +782,8 @@ size_t plan_moe(MoeArgs* a, char* base, size_t* counter_bytes) {
   // experts are one row block, whose weights are read once (more rows repeat the
   // reads, mostly out of a cache), while the rows' share of LDS stays small: it
   // decides how many workgroups a CU holds and so the weight bytes in flight
-  // (16 tokens over 8 experts of 4096 x 14336, MXFP4: blocks of 8 rows instead
-  // of 16, 219 -> 210 us).
+  // (16 tokens over 8 experts of 4096 x 14336, MXFP4: blocks of 16 rows 203 us, of
+  // 8 183).
   const int slots = (int)std::min<size_t>((size_t)a->E, P);
   int block = 8;
   while (block < 32 && (size_t)block * a->E < 2 * P) block *= 2;
@@ -794,10 +794,9 @@ size_t plan_moe(MoeArgs* a, char* base, size_t* counter_bytes) {
   // x's chunks of 512 k) need fewer column tiles.  Eight waves (four where a
   // wave's registers leave two per SIMD); fewer columns and more k while the
   // workgroups are fewer than the CUs.  Measured (us for the layer): 4 tokens
-  // over 32 experts of 2048 x 1024, MXFP4, gate_up c4k2 33.8, c1k4 40.6; one
-  // token, 64 experts, 4-bit tiled c2k4 31.6, c4k2 34.9; 33 tokens, 8-bit
-  // checkpoint layout c1k4 181, c2k4 218; 16 tokens, down c8k1 with 8 splits (one
-  // workgroup per CU, one round) 220, c4k1 with 8 (two rounds) 266.
+  // over 32 experts of 2048 x 1024, MXFP4, gate_up c4k2 27, c1k4 35; one token, 64
+  // experts, 4-bit tiled c2k4 29.5, c4k2 30.7; 33 tokens, 8-bit checkpoint layout
+  // c1k4 166, c2k4 202; 16 tokens, MXFP4, down c4k2 183, c8k1 182, c4k1 203.
   const int ku = unit_of(a->gate_up, 2), kd = unit_of(a->down, 1);
   const int uc = 16 * segment_tiles(a->gate_up.bits, a->gate_up.tiled != 0);
   const int dc = 16 * segment_tiles(a->down.bits, a->down.tiled != 0);
@@ -810,7 +809,7 @@ size_t plan_moe(MoeArgs* a, char* base, size_t* counter_bytes) {
   while (up_lds(*a) > kMoeLds && u.nwk * ku > 512) u.nwk /= 2;
   while (up_lds(*a) > kMoeLds && u.nwc > 1) u.nwc /= 2;
   // (no k wave without a unit of an expert: 5 tokens over 45 experts of 2944 x
-  // 512, 2 bits, c4k1 65, c2k4 78)
+  // 512, 2 bits, c4k1 50, c2k4 68)
   d.nwk = a->down.bits ? 4 : 2;
   while (d.nwk * kd > 512 && d.nwk / 2 * kd >= a->I) d.nwk /= 2;
   d.nwc = 8 / d.nwk;

@@ -251,15 +251,15 @@ size_t plan_mx_gemm(MxGemmArgs* a, bool allow_split, size_t* counter_bytes) {
   a->splits = 1;
   const bool mx = a->x_type == kTypeMxfp4;
   // 16-bit x of more than 32 rows: the staged rows leave no LDS for weights in
-  // flight (64 rows of 12288 x 4096: 91 us here, 30 as tiles)
+  // flight (64 rows of 12288 x 4096: 91 us that way, 21 as tiles)
   if (a->M <= (mx ? 64 : 32)) {
     // column and k waves per workgroup, measured on MI355X (us; c4k2: four
     // column waves by two k waves; s4: four workgroups along K per tile).
-    // 16-bit x: one row, 12288 x 4096 c1k4 9.1, c2k2 10.1; 28672 x 8192 c1k4 30,
-    // c4k2 30.  Sixteen rows, 12288 x 4096 c4k2 12.9, c1k4 30; 4096 x 11008 c4k2
-    // s4 14.9, s2 18.2.  More column waves share each staged row of x.  MXFP4 x,
-    // 12288 x 4096: one row c2k2 7.9, c1k4 10.3; 17 rows c2k2 9.4, c4k2 10.1; 64
-    // rows c4k2 13.9, c4k1 15.5.
+    // 16-bit x: one row, 12288 x 4096 c1k4 8.1, c2k2 8.2; 28672 x 8192 c1k4 31.1,
+    // c4k2 28.7.  Sixteen rows, 12288 x 4096 c4k2 11.9, c1k4 34; 4096 x 11008 c4k2
+    // s4 12.8, s2 16.9.  More column waves share each staged row of x.  MXFP4 x,
+    // 12288 x 4096: one row c2k2 6.7, c1k4 8.1; 17 rows c2k2 8.6, c4k2 8.8; 64
+    // rows c4k2 14.0, c4k1 16.0.
     const int units = (a->K + 511) / 512;
     if (mx) {
       a->nwc = a->M <= 32 ? 2 : 4;
@@ -283,10 +283,11 @@ size_t plan_mx_gemm(MxGemmArgs* a, bool allow_split, size_t* counter_bytes) {
   // Tiles: rows per tile and splits of K by a time model (us) of the measured
   // times: k tiles in a row, times the workgroups a CU takes in turn, plus a
   // split's fixed cost and its partial sums' traffic.  16-bit x: 0.9 per k tile of
-  // 128 rows and 0.72 of 64 (512 x 22016 x 4096: 108 and 137 us; 256-row tiles, one
-  // wave per SIMD, were slower or equal everywhere); MXFP4: 1 per
-  // k tile of 128 x 128, two workgroups to a CU, and 2.6 of 256 x 256 (2048 x
-  // 28672 x 8192: 380 and 318 us; 700 x 5000 x 4096: 18 and 38).
+  // 128 rows and 0.72 of 64 (512 x 22016 x 4096: 101 and 119 us; 64 x 12288 x 4096
+  // takes 21.5 where the model says 17.6; 256-row tiles, one wave per SIMD, were
+  // slower or equal everywhere); MXFP4: 1 per k tile of 128 x 128, two workgroups
+  // to a CU, and 2.6 of 256 x 256 (2048 x 28672 x 8192: 376 and 306 us; 700 x 5000 x
+  // 4096: 16 and 32).
   const int kt = mx ? 256 : 64, ktiles = (a->K + kt - 1) / kt;
   a->pair_stores = a->N % 2 == 0;
   a->quad_stores = (reinterpret_cast<uintptr_t>(a->out) & 15) == 0;

@@ -249,7 +249,7 @@ template <bool BF16, int BM> __global__ __launch_bounds__(256, 2) void mx_tile_k
 // each W x W matrix-instruction tiles.  Rows of x and of W both go through LDS
 // (a wave's own rows straight into registers meet 64 cache lines per load, 16
 // bytes of each, and then bound the kernel: 346 us at 2048 x 28672 x 8192, with
-// W = 4, for 318 now), S stages, S - 1 k tiles ahead: two where two workgroups
+// W = 4, for 306 to 317 now), S stages, S - 1 k tiles ahead: two where two workgroups
 // share a CU or the tile is large, four where there is at most a workgroup per
 // CU (333 x 4096 x 11008: 22 us with four, 24 with two).  Half h of a wave
 // takes blocks 4 h + s in step s, so a lane's four scale bytes are one dword;
