@@ -122,13 +122,15 @@ def test_zero_nan_and_infinite_fp16_tokens_stay_in_their_row(dev, T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [4, 5, 64, 66, 70, 130])
+@pytest.mark.parametrize("T,I,k", [(4, 96, 3), (21, 96, 3), (22, 96, 3), (64, 96, 1), (16, 1024, 4), (16, 1056, 4),
+                                   (66, 96, 3), (70, 96, 3), (130, 96, 3)])
 @pytest.mark.parametrize("bits,tiled", [(4, True), (8, False)])
-def test_token_counts_around_the_ways_h_is_split(dev, T, bits, tiled):
-    """Up to four tokens, more, several launches, and a last launch of either kind."""
-    y, ref, bound, _, (x, wr, k, s1, s2) = layer(dev, T, 128, 96, 6, 3, bits, tiled, "fp16", 0.25, 2.0, False, seed=T)
+def test_sizes_around_the_ways_h_is_split(dev, T, I, k, bits, tiled):
+    """Rows (64) and values (65536) at the limit and beyond, several launches, a last launch of either kind."""
+    y, ref, bound, _, (x, wr, k, s1, s2) = layer(dev, T, 128, I, 6, k, bits, tiled, "fp16", 0.25, 2.0, False, seed=T)
     assert_within(y, ref, bound)
-    assert torch.equal(gq.moe_layer(x, wr, k, s1, s2, renormalize=False), gq.moe_layer(x, wr, k, s1, s2, renormalize=False))
+    assert torch.equal(gq.moe_layer(x, wr, k, s1, s2, renormalize=False),
+                       gq.moe_layer(x, wr, k, s1, s2, renormalize=False))
 
 
 @pytest.mark.gpu

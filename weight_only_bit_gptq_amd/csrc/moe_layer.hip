@@ -196,12 +196,13 @@ __device__ __forceinline__ void split_store(uint16_t* hi, uint16_t* lo, float v)
 // every value, or 2^-39 of the row's largest.  The flush undoes the scale.  (A
 // value per tile and not one raised by atomics: one token over 64 experts of 2048
 // x 1024, gate_up 9.5 us and 13.5, 64 atomics meeting at an address.)
-// Up to kWideTokens tokens are split by the down product in LDS, every column tile
-// anew; more by a kernel of its own first (us for the layer,
-// without it and with it: one token, 64 experts of 2048 x 1024, k 8, 27.8 and
-// 30.9; four tokens 50 and 52; 16 tokens, 8 experts of 4096 x 14336, k 2, 245
-// and 220; 64 tokens, 16 experts of 2048 x 2048, k 16, 443 and 279).
-constexpr int kWideTokens = 4;
+// Few values (up to kWidePairs rows and kWideValues values) are split by the down
+// product in LDS, every column tile anew; more by a kernel of its own first (us for
+// the layer, without it and with it: one token, 64 experts of 2048 x 1024, k 8,
+// 28.3 and 31.1; 5 tokens, 13 experts of 3840 x 256, k 4, 31.4 and 33.8; 32 tokens,
+// 16 experts of 2048 x 1024, k 2, 54.6 and 56.2; 8 tokens, 8 experts of 4096 x 14336,
+// k 2, 200 and 189; 64 tokens, 16 experts of 2048 x 2048, k 16, 443 and 279).
+constexpr int kWidePairs = 64, kWideValues = 1 << 16;
 constexpr int kTopExponent = 14, kMostScale = 60;
 __device__ __forceinline__ int row_scale(uint32_t top) {
   return min(kTopExponent + 127 - (int)(top >> 23), kMostScale);
@@ -496,7 +497,7 @@ __global__ __launch_bounds__(512, 2) void moe_down_kernel(MoeArgs a) {
   __shared__ int16_t sorted[kMaxPairs], place[kMaxPairs];
   __shared__ int flag;
   static_assert(kMaxPairs <= kMaxExperts, "factor in count's place");
-  static_assert(kWideTokens * kMaxTopK <= 64, "WIDE: as many tokens, few pairs");
+  static_assert(kWidePairs <= 64, "WIDE: the pairs are few");
   float* factor = reinterpret_cast<float*>(count); // once sorted: what a pair's sums are multiplied by,
   int16_t* scale = place;                          // and the exponent of its row's scale (WIDE)
   constexpr int MT = 1;
@@ -834,7 +835,7 @@ size_t plan_moe(MoeArgs* a, char* base, size_t* counter_bytes) {
   a->top = reinterpret_cast<uint32_t*>(take(P * (size_t)a->up_tiles * 4));
   a->h = take(P * (size_t)a->I * 4);
   const bool fp16_parts = !a->bf16 && a->down.bits != 0;
-  a->split_first = fp16_parts && a->T > kWideTokens;
+  a->split_first = fp16_parts && (P > (size_t)kWidePairs || P * (size_t)a->I > (size_t)kWideValues);
   a->split_h = reinterpret_cast<uint16_t*>(take(a->split_first ? P * (size_t)a->I * 4 : 0));
   a->part = reinterpret_cast<float*>(take(a->splits > 1 ? (size_t)a->splits * T * (size_t)a->H * 4 : 0));
   return off;
