@@ -118,10 +118,18 @@ __device__ __forceinline__ void mx_tile_body(const MxGemmArgs& a) {
   auto compute = [&](int kt, auto st) __attribute__((always_inline)) {
     constexpr int s3 = decltype(st)::value;
     const uint8_t* sl = stage(st);
+    if constexpr (BF16) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (BF16) top = max(top, ws[s3][j]);
-      else fits = fits && (mx_fits_f16(ws[s3][j]) || mx_zero(w[s3][j]) || 2 * (kt0 + kt) + h >= w_end);
+      for (int j = 0; j < NT; ++j) top = max(top, ws[s3][j]);
+    } else {
+      bool inside = true;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) inside = inside && mx_fits_f16(ws[s3][j]);
+      if (!__all(inside)) {                        // ordinary weights do not come here
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          fits = fits && (mx_fits_f16(ws[s3][j]) || mx_zero(w[s3][j]) || 2 * (kt0 + kt) + h >= w_end);
+      }
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {

@@ -89,11 +89,15 @@ template <int T> struct MxTiles {
       }
     }
   }
-  // scale byte of block 4 j + q of the lane's row: 127 past the row's end, where a
-  // word may hold the next row's bytes, and in rows past N, where it reads as 0
-  // (outside fp16's range: 16 rows of fp16 x, 4095 x 11008, 17.7 us, and 11.9)
+  // scale byte of block 4 j + q of the lane's row: 127 past the row's end,
+  // where a word may hold the next row's bytes
   __device__ __forceinline__ uint32_t byte_of(const Regs& r, int t, int j, int unit) const {
-    return row0[t] + n < rows && 16u * (uint32_t)unit + 4 * j + q < blocks ? (r.s[t][j] >> shift) & 0xFFu : 127u;
+    return 16u * (uint32_t)unit + 4 * j + q < blocks ? (r.s[t][j] >> shift) & 0xFFu : 127u;
+  }
+  // and in rows past N, where it reads as 0: outside fp16's range (16 rows of fp16
+  // x, 4095 x 11008, 17.7 us, and 11.9)
+  __device__ __forceinline__ uint32_t byte_inside(const Regs& r, int t, int j, int unit) const {
+    return row0[t] + n < rows ? byte_of(r, t, j, unit) : 127u;
   }
   // the 16 bytes of block 4 j + q of the lane's row
   __device__ __forceinline__ u32x4_t block(const uint8_t* lds, int t, int j) const {
@@ -165,7 +169,7 @@ template <bool BF16, int CT> struct MxWeights : MxTiles<CT> {
     for (int t = 0; t < CT; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        b[t][j] = this->byte_of(r, t, j, unit);
+        b[t][j] = BF16 ? this->byte_of(r, t, j, unit) : this->byte_inside(r, t, j, unit);
         if (BF16) top = max(top, b[t][j]);
         else fits = fits && mx_fits_f16(b[t][j]);
       }
