@@ -32,16 +32,16 @@
  * synchronisation.  The library's own device memory: a workspace per
  * (device, stream) -- split-K partial sums and arrival counters, the gathered
  * x of gptq_gemm_sorted, the choices and hidden values of gptq_moe_layer --
- * allocated (hipMalloc, zeroed on the
- * stream) by the first call on that stream that needs it, and replaced by a
- * larger one when a later call needs more; a replaced buffer is not freed
+ * allocated (hipMalloc, zeroed on the stream) by the first call on that stream
+ * that needs it, and replaced by a larger one when a later call needs more; a
+ * replaced buffer is not freed
  * until gptq_release, because work queued earlier and graphs captured earlier
  * on that stream keep its address.  gptq_quantize uses a stream-ordered
  * temporary freed on the same stream.
  * HIP graphs: calls on one stream may be captured.  A capture never allocates
  * (a split-K call captured before its stream has a workspace runs unsplit
- * instead; gptq_gemm_sorted and gptq_moe_layer return GPTQ_ERR_NO_MEM), and the graph keeps
- * using the workspace its capture stream had at capture time.  So a replay
+ * instead; gptq_gemm_sorted and gptq_moe_layer return GPTQ_ERR_NO_MEM), and the
+ * graph keeps using the workspace its capture stream had at capture time.  So a replay
  * shares that workspace with every other call on the capture stream: replays
  * (on any stream) must not overlap such calls or each other, and
  * gptq_release must not run while such a graph may still replay.
